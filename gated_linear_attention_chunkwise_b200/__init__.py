@@ -8,17 +8,21 @@ importing this package fails if the library has not been built
 (`python gated_linear_attention_chunkwise_b200/build.py`).
 
 Names follow the C ABI: gla_fwd, gla_fwd_glogit, gla_fwd_f32, gla_bwd, gla_bwd_f32, gla_norm_fwd,
-gla_norm_fwd_f32, srem_reorient, dwconv3x3,
+gla_norm_fwd_f32, srem_reorient, dwconv3x3, glr_fwd, glr_fwd_packed, glr_bwd, glr_bwd_packed, glr_step, rope,
+qk_norm_rope, qk_norm_rope_bwd,
 device_status (dig_gla_device_status), status_string (dig_gla_status_string).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
 
-__all__ = ["gla_fwd", "gla_fwd_glogit", "gla_fwd_f32", "gla_bwd", "gla_bwd_f32", "gla_norm_fwd", "gla_norm_fwd_f32", "srem_reorient", "dwconv3x3", "device_status", "status_string",
+__all__ = ["gla_fwd", "gla_fwd_glogit", "gla_fwd_f32", "gla_bwd", "gla_bwd_f32", "gla_norm_fwd", "gla_norm_fwd_f32", "srem_reorient", "dwconv3x3",
+           "glr_fwd", "glr_fwd_packed", "glr_bwd", "glr_bwd_packed", "glr_step", "rope", "qk_norm_rope", "qk_norm_rope_bwd",
+           "rope_frequencies", "device_status", "status_string",
            "GlaError", "lib", "LIB_PATH", "DIR_L2R", "DIR_R2L", "DIR_T2B", "DIR_B2T"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdig_gla.so")
@@ -37,6 +41,17 @@ _lib.gla_norm_fwd.argtypes = [_vp] * 3 + [_i] * 7 + [ctypes.c_float, _vp, _u]
 _lib.gla_norm_fwd_f32.argtypes = [_vp] * 3 + [_i] * 7 + [ctypes.c_float, _vp, _u]
 _lib.srem_reorient.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _u]
 _lib.dwconv3x3.argtypes = [_vp, _vp, _i, _i, _i, _i, _i, _vp, _u]
+_i64, _f = ctypes.c_int64, ctypes.c_float
+_lib.glr_fwd.argtypes = [_vp] * 3 + [_i] * 4 + [_i64] * 2 + [_i, _f, _i, _i] + [_vp] * 2 + [_u]
+_lib.glr_fwd_packed.argtypes = [_vp] * 4 + [_i64] + [_i] * 2 + [_i64] * 2 + [_i, _f, _i, _i, _i] + [_vp] * 2 + [_u]
+_lib.glr_bwd.argtypes = [_vp] * 6 + [_i] * 4 + [_i64] * 2 + [_i, _f, _i, _i] + [_vp] * 3 + [_u]
+_lib.glr_bwd_packed.argtypes = [_vp] * 7 + [_i64] + [_i] * 2 + [_i64] * 2 + [_i, _f, _i, _i, _i] + [_vp] * 3 + [_u]
+_lib.glr_step.argtypes = [_vp] * 4 + [_i] * 3 + [_i64] * 2 + [_f, _i, _i, _i] + [_vp] * 2 + [_u]
+_lib.rope.argtypes = [_vp] * 3 + [_i] * 2 + [_vp, _i64] + [_i] * 4 + [_i64] * 2 + [_i] * 2 + [_f, _i] + [_vp, _i64] * 2 + [_u]
+_lib.qk_norm_rope.argtypes = ([_vp] * 5 + [_i] * 2 + [_vp, _i64] + [_i] * 4 + [_i64] * 2 + [_i, _f, _f, _i] + [_vp, _i64] * 2 +
+                              [_u])
+_lib.qk_norm_rope_bwd.argtypes = ([_vp] * 7 + [_i] * 2 + [_vp, _i64] + [_i] * 4 + [_i64] * 4 + [_i, _f, _f, _i] +
+                                  [_vp, _i64] * 2 + [_vp] * 2 + [_u])
 _lib.dig_gla_device_status.argtypes = [_u]
 _lib.dig_gla_status_string.argtypes = [_i]
 _lib.dig_gla_status_string.restype = ctypes.c_char_p
@@ -45,7 +60,8 @@ _lib.dig_gla_release.restype = None
 _lib.dig_gla_test_skip_items.argtypes = [_i]
 _lib.dig_gla_test_skip_items.restype = None
 for _fn in (_lib.gla_fwd, _lib.gla_fwd_glogit, _lib.gla_fwd_f32, _lib.gla_bwd, _lib.gla_bwd_f32, _lib.gla_norm_fwd, _lib.gla_norm_fwd_f32,
-            _lib.srem_reorient, _lib.dwconv3x3, _lib.dig_gla_device_status):
+            _lib.srem_reorient, _lib.dwconv3x3, _lib.glr_fwd, _lib.glr_fwd_packed, _lib.glr_bwd, _lib.glr_bwd_packed,
+            _lib.glr_step, _lib.rope, _lib.qk_norm_rope, _lib.qk_norm_rope_bwd, _lib.dig_gla_device_status):
     _fn.restype = ctypes.c_int
 
 DIR_L2R, DIR_R2L, DIR_T2B, DIR_B2T = 0, 1, 2, 3
@@ -262,6 +278,363 @@ def dwconv3x3(x, w, out=None, stream=None):
                             _stream_handle(x.device, stream))
     _check("dwconv3x3", rc)
     return out
+
+
+# ---- gated linear recurrence (vector state) -----------------------------------------
+
+
+def _row_stride(t: torch.Tensor, name: str, lead: int) -> int:
+    """Elements between token rows of t, whose first `lead` dimensions are tokens (batches
+    behind one another without a gap) and whose other dimensions are dense."""
+    inner = 1
+    for d in range(t.dim() - 1, lead - 1, -1):
+        if t.shape[d] != 1 and t.stride(d) != inner:
+            raise ValueError(f"{name}: the channels of a token must be contiguous")
+        inner *= t.shape[d]
+    step, tokens = None, 1
+    for d in range(lead - 1, -1, -1):
+        if t.shape[d] != 1:
+            if step is None:
+                step = t.stride(d)
+            elif t.stride(d) != step * tokens:
+                raise ValueError(f"{name}: its tokens must be equally spaced in memory")
+        tokens *= t.shape[d]
+    return inner if step is None else step
+
+
+def _on(t, name: str, dtype: torch.dtype, dev: torch.device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != dev or dev.type != "cuda":
+        raise ValueError(f"{name} must be on {dev if dev.type == 'cuda' else 'a CUDA device'} (got {t.device})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+
+
+def _ptr(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _call(fn: str, dev: torch.device, stream, *args):
+    if dev.index == torch.cuda.current_device():
+        rc = getattr(_lib, fn)(*args, _stream_handle(dev, stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(_lib, fn)(*args, _stream_handle(dev, stream))
+    _check(fn, rc)
+
+
+def _like(t, name: str, shape, dtype: torch.dtype, dev: torch.device):
+    """A dense output: the caller's `t`, or a new tensor."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, dtype, dev)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+    return t
+
+
+def _optional(t, name: str, shape, dev: torch.device):
+    """An optional dense fp32 input."""
+    if t is not None:
+        _need(t, name, torch.float32, dev)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+
+
+def _gated(x, gate, gate_norm, dims: int):
+    """Checks x and gate; (dtype code, gate_norm for the C call, their row strides)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dt = _grid_dtype(x)
+    _on(x, "x", x.dtype, x.device)
+    if gate_norm is not None and not (0.0 < gate_norm < math.inf):
+        raise ValueError("gate_norm must be positive and finite (None: gate holds log_alpha)")
+    _on(gate, "gate", torch.float32 if gate_norm is None else x.dtype, x.device)
+    if x.dim() != dims or gate.shape != x.shape:
+        raise ValueError(f"expected x and gate of the same {dims}-dimensional shape")
+    if max(x.shape) >= 1 << 31:
+        raise ValueError("x: a dimension of 2^31 or more")
+    return dt, 0.0 if gate_norm is None else float(gate_norm), _row_stride(x, "x", dims - 1), _row_stride(gate, "gate", dims - 1)
+
+
+def _glr_where(x, where):
+    """(leading C arguments, sequences, packed?) of a grid (Hgrid, Wgrid) or of cu_seqlens."""
+    if len(where) == 2:
+        B, T, C = x.shape
+        Hgrid, Wgrid = where
+        if T != Hgrid * Wgrid:
+            raise ValueError(f"T={T} does not match the grid {Hgrid}x{Wgrid}")
+        return (B, Hgrid, Wgrid, C), B
+    cu, = where
+    _need(cu, "cu_seqlens", torch.int32, x.device)
+    if cu.dim() != 1 or cu.numel() < 2:
+        raise ValueError("cu_seqlens must be [sequences + 1]")
+    return (x.shape[0], cu.numel() - 1, x.shape[1]), cu.numel() - 1
+
+
+def _glr_fwd(fn, x, gate, where, direction, gate_norm, complement, h0, out, h_last, stream):
+    packed = len(where) == 1
+    dt, norm, xs, gs = _gated(x, gate, gate_norm, 2 if packed else 3)
+    sizes, n = _glr_where(x, where)
+    dev, C = x.device, x.shape[-1]
+    _optional(h0, "h0", (n, C), dev)
+    fill = (int(out is None),) if packed else ()
+    out = _like(out, "out", x.shape, x.dtype, dev)
+    h_last = _like(h_last, "h_last", (n, C), torch.float32, dev)
+    _call(fn, dev, stream, x.data_ptr(), gate.data_ptr(), *map(_ptr, where[:packed]), _ptr(h0), *sizes, xs, gs,
+          int(direction), norm, int(bool(complement)), dt, *fill, out.data_ptr(), h_last.data_ptr())
+    return out, h_last
+
+
+def glr_fwd(x, gate, Hgrid: int, Wgrid: int, direction: int, gate_norm: float | None = None, complement: bool = False,
+            h0=None, out=None, h_last=None, stream=None):
+    """Gated linear recurrence h_p = alpha_p h_{p-1} + s_p x_p over the scan order of a grid (see
+    include/dig_gla.h, glr_fwd).  x [B,T,C] bf16 or fp32, possibly a slice of a wider projection;
+    gate [B,T,C]: log_alpha in fp32 (gate_norm None), or logits of x's type with log_alpha =
+    logsigmoid(gate) / gate_norm.  complement: s = 1 - alpha instead of 1.  h0 [B,C] fp32.
+    Returns (out [B,T,C], h_last [B,C] fp32); h_last may be given as h0 to carry a state in place."""
+    return _glr_fwd("glr_fwd", x, gate, (Hgrid, Wgrid), direction, gate_norm, complement, h0, out, h_last, stream)
+
+
+def glr_fwd_packed(x, gate, cu_seqlens, direction: int = 0, gate_norm: float | None = None, complement: bool = False,
+                   h0=None, out=None, h_last=None, stream=None):
+    """glr_fwd over packed sequences: x, gate [rows,C], cu_seqlens int32 [n+1] on the device,
+    direction 0 or 1, h0 and h_last [n,C].  Rows of no sequence: left as they were in a given
+    `out`, zero in a new one."""
+    return _glr_fwd("glr_fwd_packed", x, gate, (cu_seqlens,), direction, gate_norm, complement, h0, out, h_last, stream)
+
+
+def _glr_bwd(fn, x, gate, h, dout, where, direction, gate_norm, complement, h0, dh_last, outs, stream):
+    packed = len(where) == 1
+    dt, norm, xs, gs = _gated(x, gate, gate_norm, 2 if packed else 3)
+    sizes, n = _glr_where(x, where)
+    dev, C = x.device, x.shape[-1]
+    for t, name in ((h, "h"), (dout, "dout")):
+        _need(t, name, x.dtype, dev)
+        if t.shape != x.shape:
+            raise ValueError(f"{name} must have x's shape")
+    _optional(h0, "h0", (n, C), dev)
+    _optional(dh_last, "dh_last", (n, C), dev)
+    if packed and (outs[0] is None) != (outs[1] is None):
+        raise ValueError("give both dx and dgate, or neither")
+    fill = (int(outs[0] is None),) if packed else ()
+    dx = _like(outs[0], "dx", x.shape, x.dtype, dev)
+    dgate = _like(outs[1], "dgate", x.shape, gate.dtype, dev)
+    dh0 = _like(outs[2], "dh0", (n, C), torch.float32, dev)
+    _call(fn, dev, stream, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dout.data_ptr(), *map(_ptr, where[:packed]),
+          _ptr(h0), _ptr(dh_last), *sizes, xs, gs, int(direction), norm, int(bool(complement)), dt, *fill,
+          dx.data_ptr(), dgate.data_ptr(), dh0.data_ptr())
+    return dx, dgate, dh0
+
+
+def glr_bwd(x, gate, h, dout, Hgrid: int, Wgrid: int, direction: int, gate_norm: float | None = None,
+            complement: bool = False, h0=None, dh_last=None, dx=None, dgate=None, dh0=None, stream=None):
+    """The gradients of sum(dout * out) + sum(dh_last * h_last) for (out, h_last) = glr_fwd(x, gate,
+    ...), with h = that out (see include/dig_gla.h, glr_bwd).  Returns (dx of x's type, dgate of
+    gate's type, dh0 fp32 [B,C])."""
+    return _glr_bwd("glr_bwd", x, gate, h, dout, (Hgrid, Wgrid), direction, gate_norm, complement, h0, dh_last,
+                    (dx, dgate, dh0), stream)
+
+
+def glr_bwd_packed(x, gate, h, dout, cu_seqlens, direction: int = 0, gate_norm: float | None = None,
+                   complement: bool = False, h0=None, dh_last=None, dx=None, dgate=None, dh0=None, stream=None):
+    """glr_bwd over packed sequences.  Rows of no sequence: left as they were in given dx and
+    dgate, zero in new ones."""
+    return _glr_bwd("glr_bwd_packed", x, gate, h, dout, (cu_seqlens,), direction, gate_norm, complement, h0, dh_last,
+                    (dx, dgate, dh0), stream)
+
+
+def glr_step(x, gate, state, slots=None, gate_norm: float | None = None, complement: bool = False, state_out=None,
+             out=None, stream=None):
+    """One token of the recurrence for every row (see include/dig_gla.h, glr_step).  x, gate [N,C];
+    state [nslots,C] fp32; slots int32 [N] (None: row i uses state i; negative: a padded row).
+    Updates `state` in place, or writes the new states to `state_out`.  Returns (out [N,C], the
+    updated pool); padded rows are left as they were in a given `out`, zero in a new one."""
+    dt, norm, xs, gs = _gated(x, gate, gate_norm, 2)
+    dev = x.device
+    N, C = x.shape
+    _need(state, "state", torch.float32, dev)
+    if state.dim() != 2 or state.shape[1] != C:
+        raise ValueError("state must be [nslots, C]")
+    if slots is not None:
+        _need(slots, "slots", torch.int32, dev)
+        if tuple(slots.shape) != (N,):
+            raise ValueError("slots must be [N]")
+    fill = int(out is None)
+    out = _like(out, "out", (N, C), x.dtype, dev)
+    state_out = state if state_out is None else _like(state_out, "state_out", state.shape, torch.float32, dev)
+    _call("glr_step", dev, stream, x.data_ptr(), gate.data_ptr(), state.data_ptr(), _ptr(slots), N, state.shape[0], C,
+          xs, gs, norm, int(bool(complement)), dt, fill, state_out.data_ptr(), out.data_ptr())
+    return out, state_out
+
+
+# ---- rotary positions, query/key norm ------------------------------------------------
+
+
+def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
+                     original_length: int = 0, beta_fast: float = 32.0, beta_slow: float = 1.0, device=None):
+    """The inv_freq table [rot/2] (fp32) and the scale of rope and qk_norm_rope.
+
+    Unscaled, inv_freq[i] = base^(-2i/rot).  For contexts `factor` times longer than the
+    `original_length` the weights were trained on:
+      "linear"  positions shrink: inv_freq / factor
+      "base"    the base grows so that the slowest pair alone slows down by factor:
+                base * factor^(rot / (rot - 2))
+      "ramp"    pairs that turn more than beta_fast times over original_length keep their
+                frequency, those that turn less than beta_slow times are divided by
+                factor, in between the two are blended linearly in i; scale = 0.1 ln(factor) + 1
+    """
+    if rot <= 0 or rot % 2:
+        raise ValueError("rot must be positive and even")
+    if not base > 0 or not factor >= 1:
+        raise ValueError("base must be positive and factor at least 1")
+    if scaling not in (None, "linear", "base", "ramp"):
+        raise ValueError('scaling must be None, "linear", "base" or "ramp"')
+    i = torch.arange(rot // 2, dtype=torch.float64)
+    scale = 1.0
+    if scaling == "base":
+        if rot < 4:
+            raise ValueError('scaling "base" needs rot >= 4')
+        base = base * factor ** (rot / (rot - 2))
+    inv = torch.pow(torch.tensor(base, dtype=torch.float64), -2.0 * i / rot)
+    if scaling == "linear":
+        inv = inv / factor
+    elif scaling == "ramp":
+        if original_length <= 0 or not beta_fast > beta_slow > 0 or not base > 1:
+            raise ValueError('scaling "ramp" needs original_length, base > 1 and beta_fast > beta_slow > 0')
+
+        def pair_of(turns):  # the (fractional) pair that turns so often over original_length
+            return rot * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        low = max(math.floor(pair_of(beta_fast)), 0)
+        high = min(math.ceil(pair_of(beta_slow)), rot // 2 - 1)
+        slow = torch.clamp((i - low) / max(high - low, 1e-3), 0, 1)
+        inv = inv * (1 - slow) + inv / factor * slow
+        scale = 0.1 * math.log(factor) + 1.0
+    return inv.to(torch.float32).to(device or "cpu"), scale
+
+
+def _heads(t, name: str, like):
+    """Checks a tensor of heads [..., H, D]; its row stride."""
+    _on(t, name, like.dtype, like.device)
+    if t.dim() != like.dim() or t.dim() not in (3, 4) or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]:
+        raise ValueError(f"{name}: expected [rows,H,D] or [B,T,H,D] with the rows and D of the queries")
+    return _row_stride(t, name, t.dim() - 2)
+
+
+def _head_out(t, name: str, like):
+    """A caller's output of `like`'s shape, or a new dense one; with its row stride."""
+    if t is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device), like.shape[-1] * like.shape[-2]
+    s = _heads(t, name, like)
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)} (got {list(t.shape)})")
+    return t, s
+
+
+def _angles(q, positions, inv_freq):
+    """C arguments of the positions and the table, and rows, D, rot."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    _grid_dtype(q)
+    if q.dim() not in (3, 4):
+        raise ValueError("q: expected [rows,H,D] or [B,T,H,D]")
+    rows = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+            raise TypeError("positions must be an int32 or int64 tensor")
+        _need(positions, "positions", positions.dtype, q.device)
+        if positions.shape != q.shape[:-2]:
+            raise ValueError("positions must be one for each row of q")
+    rot = 0
+    if inv_freq is not None:
+        _need(inv_freq, "inv_freq", torch.float32, q.device)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot/2]")
+        rot = 2 * inv_freq.numel()
+    period = q.shape[-3]
+    return (_ptr(positions), int(positions is not None and positions.dtype == torch.int64), period, _ptr(inv_freq),
+            rows), rot
+
+
+def _rope_call(fn, q, k, weights, positions, inv_freq, middle, q_out, k_out, stream):
+    lead, rot = _angles(q, positions, inv_freq)
+    H, D = q.shape[-2:]
+    qs = _heads(q, "q", q)
+    q_out, qos = _head_out(q_out, "q_out", q)
+    ks, Hk, kos = H * D, 0, H * D
+    if k is not None:
+        ks = _heads(k, "k", q)
+        Hk = k.shape[-2]
+        k_out, kos = _head_out(k_out, "k_out", k)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    _call(fn, q.device, stream, q.data_ptr(), _ptr(k), *weights, *lead, H, Hk, D, rot, qs, ks, *middle, _grid_dtype(q),
+          q_out.data_ptr(), qos, _ptr(k_out), kos)
+    return q_out, k_out
+
+
+def rope(q, k, positions, inv_freq, interleaved: bool = False, scale: float = 1.0, inverse: bool = False, q_out=None,
+         k_out=None, stream=None):
+    """Rotary positions of query and key heads (see include/dig_gla.h, rope).  q [rows,Hq,D] or
+    [B,T,Hq,D], k likewise with Hk heads or None, bf16 or fp32, possibly slices of one fused
+    projection; positions int32/int64, one a row (None: 0..T-1 in every batch); inv_freq
+    fp32 [rot/2] (rope_frequencies).  inverse: turns back, the gradient.  q_out, k_out may be q
+    and k.  Returns (q_out, k_out)."""
+    return _rope_call("rope", q, k, (), positions, inv_freq, (int(bool(interleaved)), int(bool(inverse)), float(scale)),
+                      q_out, k_out, stream)
+
+
+def _weights(q, k, q_weight, k_weight):
+    for w, name, t in ((q_weight, "q_weight", q), (k_weight, "k_weight", k)):
+        if t is None:
+            if w is not None:
+                raise ValueError(f"{name} without its heads")
+            continue
+        _need(w, name, torch.float32, q.device)
+        if w.dim() != 1 or w.shape[0] != q.shape[-1]:
+            raise ValueError(f"{name} must be [D]")
+    return _ptr(q_weight), _ptr(k_weight)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6, interleaved: bool = False,
+                 scale: float = 1.0, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head, then rope, in one pass (see include/dig_gla.h,
+    qk_norm_rope).  q_weight, k_weight fp32 [D]; inv_freq None: the norm alone.  The rest as rope.
+    Returns (q_out, k_out)."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a torch.Tensor")
+    return _rope_call("qk_norm_rope", q, k, _weights(q, k, q_weight, k_weight), positions, inv_freq,
+                      (int(bool(interleaved)), float(eps), float(scale)), q_out, k_out, stream)
+
+
+def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6,
+                     interleaved: bool = False, scale: float = 1.0, dq=None, dk=None, stream=None):
+    """The gradients of qk_norm_rope (see include/dig_gla.h, qk_norm_rope_bwd) from its inputs and
+    those of its outputs.  dq and dk may be dq_out and dk_out.  Returns (dq, dk, dq_weight fp32,
+    dk_weight fp32)."""
+    lead, rot = _angles(q, positions, inv_freq)
+    w = _weights(q, k, q_weight, k_weight)
+    H, D = q.shape[-2:]
+    qs, dqs = _heads(q, "q", q), _heads(dq_out, "dq_out", q)
+    if dq_out.shape != q.shape:
+        raise ValueError("dq_out must have q's shape")
+    dq, dqo = _head_out(dq, "dq", q)
+    dwq = torch.empty(D, dtype=torch.float32, device=q.device)
+    Hk, ks, dks, dko, dwk = 0, H * D, H * D, H * D, None
+    if k is not None:
+        Hk, ks, dks = k.shape[-2], _heads(k, "k", q), _heads(dk_out, "dk_out", q)
+        if dk_out.shape != k.shape:
+            raise ValueError("dk_out must have k's shape")
+        dk, dko = _head_out(dk, "dk", k)
+        dwk = torch.empty(D, dtype=torch.float32, device=q.device)
+    elif dk_out is not None or dk is not None:
+        raise ValueError("dk_out or dk without k")
+    _call("qk_norm_rope_bwd", q.device, stream, dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), *w, *lead, H, Hk,
+          D, rot, dqs, dks, qs, ks, int(bool(interleaved)), float(eps), float(scale), _grid_dtype(q), dq.data_ptr(), dqo,
+          _ptr(dk), dko, dwq.data_ptr(), _ptr(dwk))
+    return dq, dk, dwq, dwk
 
 
 def skip_items_for_test(n: int) -> None:

@@ -17,9 +17,6 @@
 
 namespace dig {
 
-// Scan order codes: 0..3 the SREM orders, 4..11 the zigzag schemes.
-constexpr int kDirLast = 11;
-
 // First error a kernel recorded on this device (GLA_OK while none).
 __device__ int g_device_status = 0;
 
@@ -44,17 +41,6 @@ int check_device() {
   }
   return g_arch_ok[dev] == 1 ? GLA_OK : GLA_ERR_UNSUPPORTED;
 }
-
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
-}  // namespace
 
 int validate_gla(const void* q, const void* k, const void* v, const void* la, const void* out, int B, int H,
                  int Hg, int Wg, int dk, int dv, int dir, size_t elt) {
@@ -180,6 +166,8 @@ cudaMemPool_t workspace_pool(int dev) {
   return g_pool[dev];
 }
 
+}  // namespace
+
 int run_with_workspace(size_t bytes, cudaStream_t st, cudaError_t (*fn)(void*, void*), void* ctx) {
   void* ws = nullptr;
   if (bytes) {
@@ -196,8 +184,6 @@ int run_with_workspace(size_t bytes, cudaStream_t st, cudaError_t (*fn)(void*, v
   if (ws) cudaFreeAsync(ws, st);
   return e == cudaSuccess ? GLA_OK : GLA_ERR_CUDA;
 }
-
-}  // namespace
 
 EncodeTiledFn tensor_map_encoder() {
   static const EncodeTiledFn fn = []() -> EncodeTiledFn {  // initialised once, thread-safe

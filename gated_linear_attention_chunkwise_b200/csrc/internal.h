@@ -60,6 +60,68 @@ cudaError_t srem_reorient_launch(const void* x, void* y, int dir, int inverse, i
 cudaError_t dwconv3x3_launch(const void* x, const float* w, void* y, int B, int Hg, int Wg, int C, int dtype,
                              cudaStream_t st);
 
+// ---- gated linear recurrence (glr.cu, glr_step.cu) ----
+// A batch of grids (cu == nullptr: B sequences of Hg * Wg tokens in scan order `dir`), or
+// packed sequences (B = 1, Hg = 1, Wg = rows; sequence n is rows cu[n] .. cu[n + 1] - 1,
+// dir 0 or 1).  Strides in elements between token rows; everything else is dense.
+struct GlrArgs {
+  const void *x, *gate;
+  int64_t x_stride, gate_stride;
+  const int* cu;
+  int nseq;  // sequences: B on grids
+  int B, Hg, Wg, C, dir;
+  float gate_norm;
+  int complement, bf16;
+  int fill;            // rows outside every sequence: 1 writes zeros, 0 leaves them
+  const float* h0;     // may be null
+  void* out;           // forward
+  float* h_last;       // forward; may be null
+  const void *h, *dout;  // backward
+  const float* dh_last;  // backward; may be null
+  void *dx, *dgate;
+  float* dh0;  // may be null
+};
+cudaError_t glr_fwd_launch(const GlrArgs& a, cudaStream_t st);
+cudaError_t glr_bwd_launch(const GlrArgs& a, cudaStream_t st);
+
+struct GlrStepArgs {
+  const void *x, *gate;
+  int64_t x_stride, gate_stride;
+  const float* state;
+  float* state_out;
+  const int* slots;  // may be null: row i uses state i
+  int N, nslots, C;
+  float gate_norm;
+  int complement, bf16, fill;
+  void* out;
+};
+cudaError_t glr_step_launch(const GlrStepArgs& a, cudaStream_t st);
+
+// ---- rotary positions and the norm of query and key heads (qk_rope.cu) ----
+struct HeadRows {
+  const void* in;    // rows of H heads of D channels, `stride` elements apart
+  const void* grad;  // backward: gradient of the outputs
+  void* out;         // outputs, or the gradient of the inputs
+  int64_t stride, grad_stride, out_stride;
+  const float* weight;  // nullptr: no norm
+  float* dweight;       // backward
+  int H;
+};
+struct QkRopeArgs {
+  HeadRows q, k;  // k.H = 0: queries alone
+  const void* positions;  // int32 or int64, one for each row; nullptr: row % period
+  int positions64;
+  int period;
+  const float* inv_freq;  // rot / 2 of them
+  int64_t rows;
+  int D, rot;
+  int interleaved, inverse, bf16;
+  float eps, scale;
+};
+cudaError_t qk_rope_launch(const QkRopeArgs& a, cudaStream_t st);
+size_t qk_norm_rope_bwd_workspace_bytes(const QkRopeArgs& a);
+cudaError_t qk_norm_rope_bwd_launch(const QkRopeArgs& a, void* workspace, cudaStream_t st);
+
 // ---- test hook: work items the next bf16 GLA call leaves out (0 normally) ----
 int take_test_skip_items();
 
@@ -69,6 +131,15 @@ int check_device();
 // Argument validation of a GLA call with q/k/v/out elements of `elt` bytes.
 int validate_gla(const void* q, const void* k, const void* v, const void* la, const void* out, int B, int H, int Hg,
                  int Wg, int dk, int dv, int dir, size_t elt);
+// Runs fn(workspace, ctx) with `bytes` of stream-ordered scratch memory (none for 0).
+int run_with_workspace(size_t bytes, cudaStream_t st, cudaError_t (*fn)(void*, void*), void* ctx);
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+// Last scan order code: 0..3 the SREM orders, 4..11 the zigzag schemes.
+constexpr int kDirLast = 11;
 // Forgets the cached device address of the no-allocation scratch array (gla_noalloc.cu).
 void noalloc_forget();
 

@@ -1,7 +1,10 @@
 /*
  * dig_gla.h -- C ABI of the DiG gated-linear-attention hot path on NVIDIA B200
  * (sm_100a): the chunk-wise GLA forward over one of the four SREM scan orders,
- * the SREM reorientation of the token grid, and SREM's 3x3 depthwise conv.
+ * the SREM reorientation of the token grid, and SREM's 3x3 depthwise conv; and the
+ * operators that stand beside it in sequence models: the gated linear recurrence with
+ * a vector state (glr_*), rotary positions (rope) and the norm of query and key heads
+ * with the rotation in the same pass (qk_norm_rope*).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -45,6 +48,7 @@
 
 #include <cuda_runtime_api.h>
 #include <stddef.h>
+#include <stdint.h>
 
 #ifdef __cplusplus
 extern "C" {
@@ -52,7 +56,8 @@ extern "C" {
 
 typedef enum {
   GLA_OK = 0,
-  GLA_ERR_INVALID_ARG = -1, /* null pointer, non-positive size, bad enum, aliasing */
+  GLA_ERR_INVALID_ARG = -1, /* null pointer, non-positive size, bad enum, aliasing; in the device
+                               status: sequence lengths or state slots out of range */
   GLA_ERR_UNSUPPORTED = -2, /* a size or device this build does not handle */
   GLA_ERR_ALIGNMENT = -3,   /* a pointer or a row pitch that is not 16-byte aligned */
   GLA_ERR_CUDA = -4,        /* a CUDA runtime call failed (see cudaGetLastError) */
@@ -241,9 +246,139 @@ int dwconv3x3(const void* x, const float* w, int B, int Hgrid, int Wgrid, int C,
               cudaStream_t stream);
 
 /*
+ * The gated linear recurrence with a vector state: every channel c of every sequence is
+ * a first-order recurrence with its own data-dependent forget gate,
+ *     h_p = alpha_p h_{p-1} + s_p x_p,      out_p = h_p,      p along the scan order
+ *     alpha_p = exp(log_alpha_p)            s_p = 1, or 1 - alpha_p (complement = 1)
+ * -- gla_fwd's recurrence with a diagonal state in place of the dk x dv one.
+ *
+ *   x         rows of C channels of `dtype`; consecutive token rows are x_stride elements
+ *             apart (x_stride >= C: a slice of a wider projection), batches follow one
+ *             another without a gap.
+ *   gate      gate_norm = 0: log_alpha, fp32.  gate_norm > 0: logits of `dtype`,
+ *             log_alpha = logsigmoid(gate) / gate_norm (as gla_fwd_glogit).  Rows
+ *             gate_stride elements apart.
+ *   h0        fp32 [sequences][C], the state before the first token; NULL: zero.
+ *   out       [rows][C] of `dtype`, dense, at canonical positions.
+ *   h_last    fp32 [sequences][C], the state after the last token (unrounded; h0 for a
+ *             sequence of no token); may be NULL, may be h0 itself.
+ * C elements, x_stride and gate_stride are multiples of 16 bytes, as are all pointers
+ * (cu_seqlens, slots: 4).  Arithmetic is fp32; results in bf16 are rounded once, to
+ * nearest even.  Results do not depend on timing: repeated calls agree bit for bit.
+ * log_alpha <= 0, -inf (a full reset) included, is the domain; where growth gates
+ * multiply beyond fp32 inside the span a block works on, GLA_ERR_RANGE is recorded in
+ * the device status and the output is not valid.  NaN propagates along its channel to the
+ * end of its sequence, as in the recurrence itself.
+ *
+ * glr_fwd runs B sequences, each over the Hgrid x Wgrid grid in scan order `dir` (0..11;
+ * Hgrid = 1, dir = 0: plain token order).  No order costs copies, the zigzag ones neither.
+ */
+int glr_fwd(const void* x, const void* gate, const float* h0, int B, int Hgrid, int Wgrid, int C, int64_t x_stride,
+            int64_t gate_stride, int dir, float gate_norm, int complement, int dtype, void* out, float* h_last,
+            cudaStream_t stream);
+
+/*
+ * glr_fwd_packed -- the same over packed sequences of different lengths: sequence n is
+ * the rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 (DEVICE int32 [nseq + 1], ascending from
+ * >= 0 to <= rows; empty sequences allowed), scanned forwards (dir = 0) or backwards
+ * (dir = 1).  Rows of no sequence (padding): fill = 0 leaves their outputs as they were,
+ * fill = 1 writes zeros.  A cu_seqlens that is not ascending or leaves [0, rows] is
+ * recorded as GLA_ERR_INVALID_ARG in the device status, and the outputs are unspecified.
+ */
+int glr_fwd_packed(const void* x, const void* gate, const int* cu_seqlens, const float* h0, int64_t rows, int nseq, int C,
+                   int64_t x_stride, int64_t gate_stride, int dir, float gate_norm, int complement, int dtype,
+                   int fill, void* out, float* h_last, cudaStream_t stream);
+
+/*
+ * glr_bwd, glr_bwd_packed -- the gradients of sum(dout * out) + sum(dh_last * h_last):
+ *     d_p = dout_p + r_{p+1},   r_p = alpha_p d_p   (r behind the last token: dh_last)
+ *     dx_p = s_p d_p,   dlog_alpha_p = r_p (h_{p-1} - [complement] x_p),   dh0 = r_first
+ *   h         [rows][C] of `dtype`: the forward's `out`.  dout [rows][C] of `dtype`.
+ *   dh_last   fp32 [sequences][C]; NULL: zero.
+ *   dx        [rows][C] of `dtype`, dense.
+ *   dgate     [rows][C], dense: dlog_alpha in fp32, or the gradient of the logits,
+ *             dlog_alpha * sigmoid(-gate) / gate_norm, in `dtype`.
+ *   dh0       fp32 [sequences][C]; may be NULL, may be dh_last itself.
+ * Outputs overlap no input otherwise.  The rest as in the forward.
+ */
+int glr_bwd(const void* x, const void* gate, const void* h, const void* dout, const float* h0, const float* dh_last,
+            int B, int Hgrid, int Wgrid, int C, int64_t x_stride, int64_t gate_stride, int dir, float gate_norm,
+            int complement, int dtype, void* dx, void* dgate, float* dh0, cudaStream_t stream);
+int glr_bwd_packed(const void* x, const void* gate, const void* h, const void* dout, const int* cu_seqlens,
+                   const float* h0, const float* dh_last, int64_t rows, int nseq, int C, int64_t x_stride,
+                   int64_t gate_stride, int dir, float gate_norm, int complement, int dtype, int fill, void* dx,
+                   void* dgate, float* dh0, cudaStream_t stream);
+
+/*
+ * glr_step -- one token for each of N rows, over a pool of nslots states:
+ *     state_out[slot_i] = alpha_i state[slot_i] + s_i x_i,    out_i = state_out[slot_i]
+ *   state, state_out  fp32 [nslots][C]: the same buffer (in place) or two that do not
+ *             overlap; only the named states are written.
+ *   slots     DEVICE int32 [N]; NULL: row i uses state i.  A negative slot marks a padded
+ *             row: no state changes, its output is left (fill = 0) or zeroed (fill = 1).
+ *             A slot >= nslots counts as padding and records GLA_ERR_INVALID_ARG.  Rows
+ *             that name the same slot are its successive tokens, in row order.
+ *   x, gate   N rows as above; out [N][C] of `dtype`, dense.  N <= 65535.
+ */
+int glr_step(const void* x, const void* gate, const float* state, const int* slots, int N, int nslots, int C,
+             int64_t x_stride, int64_t gate_stride, float gate_norm, int complement, int dtype, int fill,
+             float* state_out, void* out, cudaStream_t stream);
+
+/*
+ * rope -- rotary positions of query and key heads.  Pair i of a head's first `rot`
+ * channels is turned by the angle position * inv_freq[i] and scaled:
+ *     (u, v) -> scale * (u cos - v sin, v cos + u sin)
+ *   interleaved = 0: pair i is channels (i, i + rot / 2); 1: channels (2i, 2i + 1).
+ * The other channels are copied.  inverse = 1 turns back by the same angle (and scales
+ * by the same factor): the gradient of inverse = 0.
+ *   q, k      rows of Hq (Hk) heads of D channels of `dtype`, heads dense, rows q_stride
+ *             (k_stride) elements apart: both may be slices of one fused projection.
+ *             k = NULL with Hk = 0: queries alone.
+ *   positions DEVICE int32 [rows] (positions64 = 0) or int64 (1), of any sign and size; NULL:
+ *             row r has position r mod period (rows of sequences of `period` tokens).
+ *   inv_freq  fp32 [rot / 2].  The angle is formed in fp64, so the phase of a far
+ *             position is that of the exact product.
+ *   q_out, k_out  rows like q and k with strides of their own; each may be its input (same
+ *             pointer and stride), and overlaps no input otherwise.
+ * D and rot are multiples of 8, 8 <= rot <= D <= 256; pointers and row strides are
+ * multiples of 16 bytes; rows * (Hq + Hk) <= 2^31.
+ */
+int rope(const void* q, const void* k, const void* positions, int positions64, int period, const float* inv_freq,
+         int64_t rows, int Hq, int Hk, int D, int rot, int64_t q_stride, int64_t k_stride, int interleaved, int inverse,
+         float scale, int dtype, void* q_out, int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+         cudaStream_t stream);
+
+/*
+ * qk_norm_rope -- the RMS norm of every query and key head, then rope, in one pass:
+ *     y = x / sqrt(mean(x^2) + eps) * weight   over the D channels of a head,   out = rope(y)
+ *   q_weight, k_weight  fp32 [D].  rot = 0 (inv_freq NULL): the norm alone.
+ * The rest as rope.  Arithmetic is fp32, rounded once at the end.
+ */
+int qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight, const void* positions,
+                 int positions64, int period, const float* inv_freq, int64_t rows, int Hq, int Hk, int D, int rot,
+                 int64_t q_stride, int64_t k_stride, int interleaved, float eps, float scale, int dtype, void* q_out,
+                 int64_t q_out_stride, void* k_out, int64_t k_out_stride, cudaStream_t stream);
+
+/*
+ * qk_norm_rope_bwd -- its gradients, from the inputs q, k of the forward and dq_out,
+ * dk_out (rows like q and k): with g = the turned-back gradient, r = 1 / sqrt(mean(x^2) +
+ * eps) and n = x r,
+ *     dx = r (weight g - n mean(weight g n)),      dweight = sum over rows and heads of g n
+ *   dq, dk    rows of `dtype`; each may be its dq_out (dk_out).
+ *   dq_weight, dk_weight  fp32 [D], summed in an order that does not depend on timing.
+ * Workspace: some fp32 rows of D for the weight gradients.
+ */
+int qk_norm_rope_bwd(const void* dq_out, const void* dk_out, const void* q, const void* k, const float* q_weight,
+                     const float* k_weight, const void* positions, int positions64, int period, const float* inv_freq,
+                     int64_t rows, int Hq, int Hk, int D, int rot, int64_t dq_out_stride, int64_t dk_out_stride,
+                     int64_t q_stride, int64_t k_stride, int interleaved, float eps, float scale, int dtype, void* dq,
+                     int64_t dq_stride, void* dk, int64_t dk_stride, float* dq_weight, float* dk_weight,
+                     cudaStream_t stream);
+
+/*
  * dig_gla_device_status -- synchronises `stream`, then returns and clears the
  * current device's status word: GLA_OK, or the first GLA_ERR_TIMEOUT /
- * GLA_ERR_RANGE a kernel recorded since the last call.  Returns GLA_ERR_CUDA if
+ * GLA_ERR_RANGE / GLA_ERR_INVALID_ARG a kernel recorded since the last call.  Returns GLA_ERR_CUDA if
  * the synchronisation itself fails.
  */
 int dig_gla_device_status(cudaStream_t stream);

@@ -1,0 +1,153 @@
+// glr_bwd.cu -- the gradients of the gated linear recurrence (include/dig_gla.h, glr_bwd,
+// glr_bwd_packed): the walk of glr_scan.cuh from the last token to the first.  Position j of
+// the walk is scan position T - 1 - j; what enters a span is r of the token behind it.
+#include "glr_scan.cuh"
+
+namespace dig {
+namespace glr {
+namespace {
+
+template <typename T, int kKind, bool kComp, int kLanes, int kRun>
+__global__ void __launch_bounds__(kThreads, 2) glr_bwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
+  using G = GateT<T, kKind>;
+  using RawT = typename Four<T>::Raw;
+  using RawG = typename Four<G>::Raw;
+  __shared__ Shared<kLanes> sm;
+  extern __shared__ uint4 slots[];  // gates [kRun][kThreads], then dout, h of the token before, x
+  RawG* const sg = reinterpret_cast<RawG*>(slots) + threadIdx.x;
+  RawT* const sd = reinterpret_cast<RawT*>(reinterpret_cast<RawG*>(slots) + kRun * kThreads) + threadIdx.x;
+  RawT* const sh = sd + kRun * kThreads;
+  RawT* const sx = sh + kRun * kThreads;
+
+  const int slab = blockIdx.x / cluster_size(), b = slab / slabs;
+  const int c = ((slab - b * slabs) * kLanes + threadIdx.x % kLanes) * 4;
+  const bool on = c < a.C;
+  const bool packed = a.cu != nullptr;
+  const int64_t base = (int64_t)b * g.T;
+  const int c_in = on ? c : 0;
+  const T* const x = static_cast<const T*>(a.x) + base * a.x_stride + c_in;
+  const G* const gate = static_cast<const G*>(a.gate) + base * a.gate_stride + c_in;
+  const T* const hs = static_cast<const T*>(a.h) + base * a.C + c_in;
+  const T* const dout = static_cast<const T*>(a.dout) + base * a.C + c_in;
+  T* const dx = static_cast<T*>(a.dx) + base * a.C + c;
+  G* const dgate = static_cast<G*>(a.dgate) + base * a.C + c;
+  const float inv_norm = 1.f / a.gate_norm;
+
+  F4 start = all4(0.f);
+  if (!packed && a.dh_last && on) start = load4(a.dh_last + (int64_t)b * a.C + c);
+  Walk<kLanes> walk(sm, start);
+  const int per_round = (int)walk.size * (kThreads / kLanes) * kRun;
+  int j0 = ((int)walk.rank * (kThreads / kLanes) + threadIdx.x / kLanes) * kRun;
+  int row[kRun];
+  auto load = [&](int from) {
+    Rows rows(g, g.T - 1 - from, -1);
+    int next = on && from < g.T ? rows.next() : 0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const bool there = on && from + i < g.T, before = on && from + i + 1 < g.T;
+      row[i] = next;
+      next = before ? rows.next() : 0;
+      fetch<G>(smem_u32(sg + i * kThreads), gate + row[i] * a.gate_stride, there);
+      fetch<T>(smem_u32(sd + i * kThreads), dout + (int64_t)row[i] * a.C, there);
+      fetch<T>(smem_u32(sh + i * kThreads), hs + (int64_t)next * a.C, before);
+      if constexpr (kComp) fetch<T>(smem_u32(sx + i * kThreads), x + row[i] * a.x_stride, there);
+    }
+    cp_async_commit();
+  };
+  load(j0);
+  if (packed && walk.rank == 0)
+    empty_sequences(a, g.T, c - 4 * walk.lane, 4 * kLanes, a.dh_last, a.dh0, blockIdx.x == 0);
+  cluster_wait();
+
+  bool grown = false;
+  for (int round = 0; round < rounds; ++round, j0 += per_round) {
+    const int n = on ? max(0, min(kRun, g.T - j0)) : 0;
+    // Backwards over sequences in token order the token falls by one each step.
+    Marks m{0u, 0u, 0u};
+    if (packed) m = mark(a, a.dir ? j0 : g.T - j0 - n, n, a.dir == 0);
+    cp_async_wait_all();
+    // pull = (h before - [complement] x) d log_alpha / d gate, keep = 1 - alpha.
+    F4 al[kRun], d[kRun], pull[kRun], keep[kComp ? kRun : 1];
+    Span s{all4(1.f), all4(0.f)};
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
+      F4 before = Four<T>::get(sh[i * kThreads]);
+      d[i] = Four<T>::get(sd[i * kThreads]);
+      al[i] = k.alpha;
+      if (i >= n) {
+        al[i] = all4(1.f);
+        d[i] = all4(0.f);
+      }
+      if (i < n && (packed ? (m.first >> i & 1u) : j0 + i == g.T - 1)) {
+        before = all4(0.f);
+        if (a.h0) before = load4(a.h0 + (packed ? state_row(a, row[i]) : (int64_t)b * a.C) + c);
+      }
+      if constexpr (kComp) {
+        before = sub4(before, Four<T>::get(sx[i * kThreads]));
+        keep[i] = k.rest;
+      }
+      pull[i] = kKind == kGateLog ? before : mul4(before, k.slope);
+      if (m.last >> i & 1u) {
+        if (a.dh_last) d[i] = add4(d[i], load4(a.dh_last + state_row(a, row[i]) + c));
+        s = Span{al[i], mul4(al[i], d[i])};
+      } else {
+        s = Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
+      }
+    }
+    if (any_over(s.A) || s.A.a.x != s.A.a.x || s.A.a.y != s.A.a.y || s.A.b.x != s.A.b.x || s.A.b.y != s.A.b.y) {
+      s.A = all4(1.f);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) s.A = product<false>(s.A, cap(al[i]), grown), grown |= any_over(al[i]);
+    }
+    if (m.last) s.A = all4(-0.f);
+    int at[kRun];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) at[i] = row[i];
+    if (round + 1 < rounds) load(j0 + per_round);
+    F4 r;
+    if (!(packed ? walk.template exchange<true>(s, round, r, grown) : walk.template exchange<false>(s, round, r, grown)))
+      break;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+      const F4 delta = m.last >> i & 1u ? d[i] : add4(d[i], r);
+      r = mul4(al[i], delta);
+      if (i >= n) continue;
+      F4 vx = delta, vg = mul4(r, pull[i]);
+      if constexpr (kComp) vx = mul4(delta, keep[i]);
+      if (a.dh0 && (m.first >> i & 1u)) store4(a.dh0 + state_row(a, at[i]) + c, r);
+      if (packed && !(m.inside >> i & 1u)) {
+        if (!a.fill) continue;
+        vx = vg = all4(0.f);
+      }
+      store4(dx + (int64_t)at[i] * a.C, vx);
+      store4(dgate + (int64_t)at[i] * a.C, vg);
+    }
+  }
+  cp_async_wait_all();
+  if (!packed && a.dh0 && on && walk.rank == 0 && threadIdx.x < kLanes)
+    store4(a.dh0 + (int64_t)b * a.C + c, walk.carry);
+  if (grown) report_status(GLA_ERR_RANGE);
+  walk.leave();
+}
+
+template <typename T, int kKind, bool kComp>
+struct Backward {
+  static cudaError_t run(const GlrArgs& a, cudaStream_t st) {
+    constexpr int kRun = 4;
+    const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
+    const size_t smem = (size_t)kRun * kThreads *
+                        ((kComp ? 3 : 2) * sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
+    const int64_t wide = (int64_t)a.B * ((a.C + 63) / 64);
+    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 16 * kRun)
+      return enqueue(glr_bwd_k<T, kKind, kComp, 16, kRun>, a, g, 16, kRun, 296, smem, st);
+    return enqueue(glr_bwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 296, smem, st);
+  }
+};
+
+}  // namespace
+}  // namespace glr
+
+cudaError_t glr_bwd_launch(const GlrArgs& a, cudaStream_t st) { return glr::by_types<glr::Backward>(a, st); }
+
+}  // namespace dig

@@ -1,0 +1,359 @@
+// glr_scan.cuh -- the walk that glr_fwd and glr_bwd share (glr_fwd.cu, glr_bwd.cu).
+//
+// Mathematics.  Both passes are first-order recurrences per channel: forwards
+// h_p = alpha_p h_{p-1} + u_p, backwards r_p = alpha_p (d_p + r_{p+1}).  A span of tokens
+// maps the value that enters it to A * in + h, and two spans compose to (A2 A1, A2 h1 + h2),
+// so a long sequence is cut into spans that are folded separately and then joined.
+//
+// Split.  A cluster of up to 8 blocks owns a slab of channels of one sequence (or of the
+// row of packed sequences) and walks it in rounds.  In a round every thread folds kRun
+// consecutive tokens of four channels in registers; warps join their threads' spans by
+// shuffles, the block its warps' in shared memory, the cluster its blocks' by asynchronous
+// stores into one another's shared memory; then each thread applies the value that enters
+// its span to its tokens.  Every input is read once, every output written once, nothing
+// passes between blocks through global memory, there is no workspace, and the order of
+// every sum is fixed.  A thread's tokens of the next round are copied (cp.async) into
+// slots of shared memory that only it reads while the current round is joined and written.
+//
+// Packed sequences are one long row of tokens; a span that begins a sequence forgets
+// what enters it.  That is marked by the sign bit of A (gates are never negative): the
+// fold then selects instead of multiplying by zero, so a NaN ends with its sequence.
+#pragma once
+
+#include "glr.cuh"
+
+namespace dig {
+namespace glr {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
+
+// ---- spans of four channels ---------------------------------------------------------------
+struct Span {
+  F4 A, h;
+};
+constexpr uint32_t kForget = 0x80000000u;  // sign bit of A: nothing that enters matters
+
+__device__ __forceinline__ bool forgets(float A) { return (int)__float_as_uint(A) < 0; }
+__device__ __forceinline__ bool any_over(F4 v) {  // (a NaN compares false)
+  return v.a.x > FLT_MAX || v.a.y > FLT_MAX || v.b.x > FLT_MAX || v.b.y > FLT_MAX;
+}
+__device__ __forceinline__ F4 cap(F4 v) {
+  auto c = [](float x) { return x > FLT_MAX ? FLT_MAX : x; };
+  return F4{make_float2(c(v.a.x), c(v.a.y)), make_float2(c(v.b.x), c(v.b.y))};
+}
+
+// kMarks: spans may be marked to forget (packed rows).
+template <bool kMarks>
+__device__ __forceinline__ F4 enter(const Span& s, F4 in) {
+  F4 v = fma4(s.A, in, s.h);
+  if constexpr (kMarks) {
+    v.a.x = forgets(s.A.a.x) ? s.h.a.x : v.a.x;
+    v.a.y = forgets(s.A.a.y) ? s.h.a.y : v.a.y;
+    v.b.x = forgets(s.A.b.x) ? s.h.b.x : v.b.x;
+    v.b.y = forgets(s.A.b.y) ? s.h.b.y : v.b.y;
+  }
+  return v;
+}
+// A product of gates; a mark in either factor stays.  Growth is held at the largest fp32
+// number (and reported), so that a zero that enters later gives zero instead of NaN.
+template <bool kMarks>
+__device__ __forceinline__ F4 product(F4 x, F4 y, bool& grown) {
+  F4 v = mul4(x, y);
+  if (any_over(v)) {
+    grown = true;
+    v = cap(v);
+  }
+  if constexpr (kMarks) {
+    auto m = [](float r, float p, float q) {
+      return __uint_as_float(__float_as_uint(r) | ((__float_as_uint(p) | __float_as_uint(q)) & kForget));
+    };
+    v = F4{make_float2(m(v.a.x, x.a.x, y.a.x), m(v.a.y, x.a.y, y.a.y)),
+           make_float2(m(v.b.x, x.b.x, y.b.x), m(v.b.y, x.b.y, y.b.y))};
+  }
+  return v;
+}
+template <bool kMarks>
+__device__ __forceinline__ Span join(const Span& first, const Span& then, bool& grown) {
+  return Span{product<kMarks>(first.A, then.A, grown), enter<kMarks>(then, first.h)};
+}
+
+// ---- the exchange ---------------------------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_to(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+// 16 bytes into another block's shared memory; its barrier counts them.
+__device__ __forceinline__ void store_async(uint32_t addr, uint32_t bar, F4 v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "f"(v.a.x), "f"(v.a.y), "f"(v.b.x), "f"(v.b.y), "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+template <int kLanes>
+struct Shared {
+  Span warp[2][kWarps][kLanes];        // spans of this block's warps, by parity of the round
+  Span total[2][kMaxCluster][kLanes];  // spans of the cluster's blocks
+  uint64_t bar[2];                     // total[i] has arrived
+};
+
+// One block's place and the value that runs along its slab.
+template <int kLanes>
+struct Walk {
+  Shared<kLanes>& sm;
+  uint32_t rank, size;
+  int lane, warp, seg;  // channel group in the slab; warp; the thread's span within the warp
+  F4 carry;             // the value at the start of the round
+  bool late = false;    // a wait ran out
+
+  __device__ __forceinline__ Walk(Shared<kLanes>& s, const F4& start) : sm(s), carry(start) {
+    rank = cluster_rank();
+    size = cluster_size();
+    lane = threadIdx.x % kLanes;
+    warp = threadIdx.x >> 5;
+    seg = (threadIdx.x & 31) / kLanes;
+    if (threadIdx.x == 0) {
+      mbar_init(smem_u32(&sm.bar[0]), 1);
+      mbar_init(smem_u32(&sm.bar[1]), 1);
+      fence_mbar_init();
+    }
+    cluster_arrive();  // every block runs, with its barriers set up, before one writes to another
+  }
+
+  // The value that enters this thread's span s.  Returns false, in all threads of the block
+  // alike, when an earlier round's wait ran out.
+  //
+  // Reuse of the buffers: a block sends its total of round k + 2 only after it has received
+  // all totals of round k + 1, and a block sends that only after all its threads have passed
+  // the __syncthreads of round k + 1, behind their reads of round k.
+  template <bool kMarks>
+  __device__ __forceinline__ bool exchange(const Span& s, int round, F4& in, bool& grown) {
+    const int par = round & 1;
+    Span inc = s;  // inclusive scan over the warp's spans
+#pragma unroll
+    for (int off = kLanes; off < 32; off *= 2) {
+      const Span o = shift(inc, off);
+      if ((int)(threadIdx.x & 31) >= off) inc = join<kMarks>(o, inc, grown);
+    }
+    const Span ex = shift(inc, kLanes);
+    if ((threadIdx.x & 31) >= 32 - kLanes) sm.warp[par][warp][lane] = inc;
+    if (threadIdx.x == 0) expect_bytes(smem_u32(&sm.bar[par]), size * kLanes * (uint32_t)sizeof(Span));
+    if (__syncthreads_or(late)) return false;
+    Span pre{all4(1.f), all4(0.f)};  // the warps before this one
+    for (int i = 0; i < warp; ++i) pre = i == 0 ? sm.warp[par][0][lane] : join<kMarks>(pre, sm.warp[par][i][lane], grown);
+    if (warp == kWarps - 1 && seg == 32 / kLanes - 1) {
+      const Span t = join<kMarks>(pre, inc, grown);
+      const uint32_t to = smem_u32(&sm.total[par][rank][lane]), bar = smem_u32(&sm.bar[par]);
+      for (uint32_t r = 0; r < size; ++r) {
+        const uint32_t addr = map_to(to, r), at = map_to(bar, r);
+        store_async(addr, at, t.A);
+        store_async(addr + 16u, at, t.h);
+      }
+    }
+    if (seg) pre = join<kMarks>(pre, ex, grown);
+    if (!mbar_wait(smem_u32(&sm.bar[par]), (round >> 1) & 1)) {
+      report_status(GLA_ERR_TIMEOUT);
+      late = true;
+    }
+    F4 v = carry;
+    for (uint32_t r = 0; r < size; ++r) {
+      if (r == rank) in = enter<kMarks>(pre, v);
+      v = enter<kMarks>(sm.total[par][r][lane], v);
+    }
+    carry = v;
+    return true;
+  }
+
+  // No block leaves while another may still write to it.
+  __device__ __forceinline__ void leave() {
+    cluster_arrive();
+    cluster_wait();
+  }
+
+ private:
+  static __device__ __forceinline__ Span shift(const Span& s, int by) {
+    auto f = [by](float v) { return __shfl_up_sync(0xffffffffu, v, by); };
+    return Span{F4{make_float2(f(s.A.a.x), f(s.A.a.y)), make_float2(f(s.A.b.x), f(s.A.b.y))},
+                F4{make_float2(f(s.h.a.x), f(s.h.a.y)), make_float2(f(s.h.b.x), f(s.h.b.y))}};
+  }
+};
+
+// ---- tokens -----------------------------------------------------------------------------------
+
+// Rows of scan positions p, p + step, ... (step +-1): one division, then increments.
+struct Rows {
+  const ScanGeom& g;
+  int p, step, f, x, y, df;
+
+  __device__ __forceinline__ Rows(const ScanGeom& geom, int first, int by) : g(geom), p(first), step(by) {
+    f = g.reverse ? g.T - 1 - p : p;  // position in the base order
+    df = g.reverse ? -step : step;
+    if (g.column_base) {
+      x = f / g.Hg;  // (a position before the first token is never used)
+      y = f - x * g.Hg;
+    }
+  }
+  __device__ __forceinline__ int next() {
+    int row;
+    if (g.zigzag) {
+      row = zigzag_token(g, p);
+    } else if (g.column_base) {
+      row = y * g.Wg + x;
+      y += df;
+      if (y == g.Hg) {
+        y = 0;
+        ++x;
+      } else if (y < 0) {
+        y = g.Hg - 1;
+        --x;
+      }
+    } else {
+      row = f;
+    }
+    f += df;
+    p += step;
+    return row;
+  }
+};
+
+// Four channels of a token into this thread's slot; zeros where there is no token.
+template <typename T>
+__device__ __forceinline__ void fetch(uint32_t slot, const T* p, bool there) {
+  if constexpr (sizeof(T) == 2) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(slot), "l"(p), "r"(there ? 8u : 0u) : "memory");
+  } else {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot), "l"(p), "r"(there ? 16u : 0u) : "memory");
+  }
+}
+
+// ---- packed sequences ---------------------------------------------------------------------------
+
+// Sequence of packed token t: the last n in [0, nseq) with cu[n] <= t, or -1 before all.
+__device__ __forceinline__ int find_sequence(const int* cu, int nseq, int t) {
+  int lo = 0, hi = nseq;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= t)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo - 1;
+}
+// Its row in the states, for a token that mark() found to begin or end a sequence (in range
+// whatever the lengths hold).
+__device__ __forceinline__ int64_t state_row(const GlrArgs& a, int t) {
+  return (int64_t)max(find_sequence(a.cu, a.nseq, t), 0) * a.C;
+}
+
+// Of a thread's tokens (bit i: the i-th it walks): which lie in a sequence, begin one, end
+// one (first and last in scan order).
+struct Marks {
+  uint32_t inside, first, last;
+};
+// The tokens are lo .. lo + n - 1; turned: walked from the highest to the lowest.
+__device__ __forceinline__ Marks mark(const GlrArgs& a, int lo, int n, bool turned) {
+  Marks m{0u, 0u, 0u};
+  if (n <= 0) return m;
+  int q = find_sequence(a.cu, a.nseq, lo);
+  if (q >= 0 && a.cu[q] < lo && a.cu[q + 1] > lo + n) {  // amid one sequence: the usual case
+    m.inside = (1u << n) - 1u;
+    return m;
+  }
+  for (int i = 0; i < n; ++i) {
+    const int t = lo + i;
+    while (q + 1 < a.nseq && a.cu[q + 1] <= t) ++q;
+    if (q < 0 || t >= a.cu[q + 1]) continue;
+    const uint32_t bit = 1u << (turned ? n - 1 - i : i);
+    m.inside |= bit;
+    const bool lowest = t == a.cu[q], highest = t + 1 == a.cu[q + 1];
+    if (a.dir ? highest : lowest) m.first |= bit;
+    if (a.dir ? lowest : highest) m.last |= bit;
+  }
+  return m;
+}
+
+// States of sequences of no token, which no thread reaches through its tokens, and the check
+// of the lengths (no address of a token depends on them).
+__device__ __forceinline__ void empty_sequences(const GlrArgs& a, int T, int c0, int width, const float* from, float* to,
+                                                bool checks) {
+  for (int n = threadIdx.x; n < a.nseq; n += kThreads) {
+    const int s = a.cu[n], e = a.cu[n + 1];
+    if (checks && (s < 0 || e > T || s > e)) report_status(GLA_ERR_INVALID_ARG);
+    if (s == e && to)
+      for (int c = c0; c < min(c0 + width, a.C); ++c) to[(int64_t)n * a.C + c] = from ? from[(int64_t)n * a.C + c] : 0.f;
+  }
+}
+
+// ---- launch -------------------------------------------------------------------------------------
+using Kernel = void (*)(GlrArgs, ScanGeom, int, int);
+
+// The widest cluster, up to 8, for which all blocks find room (`room` of them) and have tokens.
+inline int cluster_for(int64_t slabs, int T, int per_block, int64_t room) {
+  int c = 1;
+  while (c < kMaxCluster && slabs * c * 2 <= room && (int64_t)c * per_block < T) c *= 2;
+  return c;
+}
+
+inline cudaError_t enqueue(Kernel k, const GlrArgs& a, const ScanGeom& g, int lanes, int run, int room, size_t smem,
+                           cudaStream_t st) {
+  const int slabs = (a.C + 4 * lanes - 1) / (4 * lanes);
+  const int per_block = kThreads / lanes * run;
+  const int cluster = cluster_for((int64_t)a.B * slabs, g.T, per_block, room);
+  const int64_t per_round = (int64_t)cluster * per_block;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3((unsigned)((int64_t)a.B * slabs * cluster));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, k, a, g, slabs, (int)((g.T + per_round - 1) / per_round));
+}
+
+// Calls f<T, kind, complement>() for the call's types.
+template <template <typename, int, bool> class F, typename... Args>
+cudaError_t by_types(const GlrArgs& a, Args... args) {
+  const int kind = gate_kind(a.gate_norm);
+#define DIG_GLR(T, K, C) F<T, K, C>::run(a, args...)
+#define DIG_GLR_FORM(T, K) (a.complement ? DIG_GLR(T, K, true) : DIG_GLR(T, K, false))
+#define DIG_GLR_KIND(T)                            \
+  (kind == kGateLog ? DIG_GLR_FORM(T, kGateLog)    \
+                    : kind == kGateSigmoid ? DIG_GLR_FORM(T, kGateSigmoid) : DIG_GLR_FORM(T, kGateLogit))
+  return a.bf16 ? DIG_GLR_KIND(__nv_bfloat16) : DIG_GLR_KIND(float);
+#undef DIG_GLR_KIND
+#undef DIG_GLR_FORM
+#undef DIG_GLR
+}
+
+}  // namespace glr
+}  // namespace dig

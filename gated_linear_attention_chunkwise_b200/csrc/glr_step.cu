@@ -8,6 +8,11 @@ namespace {
 
 constexpr int kThreads = 128;
 
+__device__ __forceinline__ float load_f32(const float* p) { return *p; }
+__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
 // One thread per (row, channel).  Rows that name the same state belong together: the
 // first of them applies all, in row order, the others do nothing.
 template <typename T, int kKind>
@@ -32,9 +37,9 @@ __global__ void __launch_bounds__(kThreads) glr_step_k(GlrStepArgs a, int cblock
   float h = a.state[(int64_t)slot * a.C + c];
   for (int j = i; j < a.N; ++j) {
     if (j != i && (!a.slots || a.slots[j] != slot)) continue;
-    const Gate k = make_gate<kKind>(load_f32(gate + j * a.gate_stride + c), inv_norm);
+    const Gates k = make_gates<kKind>(both(load_f32(gate + j * a.gate_stride + c)), inv_norm);
     const float u = load_f32(x + j * a.x_stride + c);
-    h = fmaf(k.alpha, h, a.complement ? k.rest * u : u);
+    h = fmaf(k.alpha.x, h, a.complement ? k.rest.x * u : u);
     store_f32(out + (int64_t)j * a.C + c, h);
   }
   a.state_out[(int64_t)slot * a.C + c] = h;

@@ -8,7 +8,7 @@ namespace glr {
 namespace {
 
 template <typename T, int kKind, bool kComp, int kLanes, int kRun>
-__global__ void __launch_bounds__(kThreads, 2) glr_bwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
+__global__ void __launch_bounds__(kThreads, 4) glr_bwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
   using G = GateT<T, kKind>;
   using RawT = typename Four<T>::Raw;
   using RawG = typename Four<G>::Raw;
@@ -38,19 +38,39 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_k(GlrArgs a, ScanGeom g, 
   Walk<kLanes> walk(sm, start);
   const int per_round = (int)walk.size * (kThreads / kLanes) * kRun;
   int j0 = ((int)walk.rank * (kThreads / kLanes) + threadIdx.x / kLanes) * kRun;
-  int row[kRun];
+  const uint32_t slot_g = smem_u32(sg), slot_d = smem_u32(sd), slot_h = smem_u32(sh), slot_x = smem_u32(sx);
+  constexpr uint32_t kStepG = kThreads * sizeof(RawG), kStepT = kThreads * sizeof(RawT);
   auto load = [&](int from) {
     Rows rows(g, g.T - 1 - from, -1);
-    int next = on && from < g.T ? rows.next() : 0;
+    int apart;
+    if (on && from + kRun < g.T && rows.even(g, kRun + 1, apart)) {
+      const int64_t row = rows.next(g);
+      const G* pg = gate + row * a.gate_stride;
+      const T *pd = dout + row * a.C, *ph = hs + (row + apart) * a.C, *px = x + row * a.x_stride;
+      const int64_t dg = apart * a.gate_stride, dc = (int64_t)apart * a.C, ds = apart * a.x_stride;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const bool there = on && from + i < g.T, before = on && from + i + 1 < g.T;
-      row[i] = next;
-      next = before ? rows.next() : 0;
-      fetch<G>(smem_u32(sg + i * kThreads), gate + row[i] * a.gate_stride, there);
-      fetch<T>(smem_u32(sd + i * kThreads), dout + (int64_t)row[i] * a.C, there);
-      fetch<T>(smem_u32(sh + i * kThreads), hs + (int64_t)next * a.C, before);
-      if constexpr (kComp) fetch<T>(smem_u32(sx + i * kThreads), x + row[i] * a.x_stride, there);
+      for (int i = 0; i < kRun; ++i) {
+        fetch<G>(slot_g + i * kStepG, pg, true);
+        fetch<T>(slot_d + i * kStepT, pd, true);
+        fetch<T>(slot_h + i * kStepT, ph, true);
+        if constexpr (kComp) fetch<T>(slot_x + i * kStepT, px, true);
+        pg += dg;
+        pd += dc;
+        ph += dc;
+        px += ds;
+      }
+    } else {
+      int next = on && from < g.T ? rows.next(g) : 0;
+#pragma unroll 1
+      for (int i = 0; i < kRun; ++i) {
+        const bool there = on && from + i < g.T, before = on && from + i + 1 < g.T;
+        const int64_t row = next;
+        next = before ? rows.next(g) : 0;
+        fetch<G>(slot_g + i * kStepG, gate + row * a.gate_stride, there);
+        fetch<T>(slot_d + i * kStepT, dout + row * a.C, there);
+        fetch<T>(slot_h + i * kStepT, hs + (int64_t)next * a.C, before);
+        if constexpr (kComp) fetch<T>(slot_x + i * kStepT, x + row * a.x_stride, there);
+      }
     }
     cp_async_commit();
   };
@@ -60,68 +80,94 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_k(GlrArgs a, ScanGeom g, 
   cluster_wait();
 
   bool grown = false;
+  Amid amid;
   for (int round = 0; round < rounds; ++round, j0 += per_round) {
     const int n = on ? max(0, min(kRun, g.T - j0)) : 0;
     // Backwards over sequences in token order the token falls by one each step.
     Marks m{0u, 0u, 0u};
-    if (packed) m = mark(a, a.dir ? j0 : g.T - j0 - n, n, a.dir == 0);
+    if (packed) m = mark(a, a.dir ? j0 : g.T - j0 - n, n, a.dir == 0, amid);
+    if (!packed && n > 0 && j0 + n == g.T) m.first = 1u << (n - 1);  // the scan's first token
     cp_async_wait_all();
     // pull = (h before - [complement] x) d log_alpha / d gate, keep = 1 - alpha.
     F4 al[kRun], d[kRun], pull[kRun], keep[kComp ? kRun : 1];
-    Span s{all4(1.f), all4(0.f)};
+    Span s = nothing();
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
       F4 before = Four<T>::get(sh[i * kThreads]);
       d[i] = Four<T>::get(sd[i * kThreads]);
       al[i] = k.alpha;
-      if (i >= n) {
-        al[i] = all4(1.f);
-        d[i] = all4(0.f);
-      }
-      if (i < n && (packed ? (m.first >> i & 1u) : j0 + i == g.T - 1)) {
+      if (m.first >> i & 1u) {
         before = all4(0.f);
-        if (a.h0) before = load4(a.h0 + (packed ? state_row(a, row[i]) : (int64_t)b * a.C) + c);
+        if (a.h0) {
+          Rows rows(g, g.T - 1 - (j0 + i), -1);
+          before = load4(a.h0 + (packed ? state_row(a, rows.next(g)) : (int64_t)b * a.C) + c);
+        }
       }
       if constexpr (kComp) {
         before = sub4(before, Four<T>::get(sx[i * kThreads]));
         keep[i] = k.rest;
       }
       pull[i] = kKind == kGateLog ? before : mul4(before, k.slope);
-      if (m.last >> i & 1u) {
-        if (a.dh_last) d[i] = add4(d[i], load4(a.dh_last + state_row(a, row[i]) + c));
-        s = Span{al[i], mul4(al[i], d[i])};
-      } else {
-        s = Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
+      s = i == 0 ? Span{al[0], mul4(al[0], d[0])} : Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
+    }
+    // Tokens that are missing or end a sequence, growth, and NaN gates are folded again.
+    const bool plain = n == kRun && m.last == 0u;
+    bool odd = !all_within(s.A, 1.f);
+    if (!plain || odd) {
+      s = nothing();
+      Rows rows(g, g.T - 1 - j0, -1);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (i >= n) {
+          al[i] = all4(1.f);
+          d[i] = all4(0.f);
+        }
+        const int row = i < n ? rows.next(g) : 0;
+        if (m.last >> i & 1u) {
+          if (a.dh_last) d[i] = add4(d[i], load4(a.dh_last + state_row(a, row) + c));
+          s = Span{all4(1.f), mul4(al[i], d[i])};
+        } else {
+          s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), mul4(al[i], add4(d[i], s.h))};
+        }
       }
+      odd = m.last != 0u || !all_within(s.A, 1.f);
+      if (m.last) s.A.a.x = -0.f;
     }
-    if (any_over(s.A) || s.A.a.x != s.A.a.x || s.A.a.y != s.A.a.y || s.A.b.x != s.A.b.x || s.A.b.y != s.A.b.y) {
-      s.A = all4(1.f);
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) s.A = product<false>(s.A, cap(al[i]), grown), grown |= any_over(al[i]);
-    }
-    if (m.last) s.A = all4(-0.f);
-    int at[kRun];
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) at[i] = row[i];
     if (round + 1 < rounds) load(j0 + per_round);
     F4 r;
-    if (!(packed ? walk.template exchange<true>(s, round, r, grown) : walk.template exchange<false>(s, round, r, grown)))
-      break;
+    if (!walk.exchange(s, odd, packed, round, r, grown)) break;
+    Rows rows(g, g.T - 1 - j0, -1);
+    int apart;
+    if (plain && (!packed || m.first == 0u) && rows.even(g, kRun, apart) && (!packed || m.inside == (1u << kRun) - 1u)) {
+      const int64_t row = rows.next(g), step = (int64_t)apart * a.C;
+      T* px = dx + row * a.C;
+      G* pg = dgate + row * a.C;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const F4 delta = m.last >> i & 1u ? d[i] : add4(d[i], r);
-      r = mul4(al[i], delta);
-      if (i >= n) continue;
-      F4 vx = delta, vg = mul4(r, pull[i]);
-      if constexpr (kComp) vx = mul4(delta, keep[i]);
-      if (a.dh0 && (m.first >> i & 1u)) store4(a.dh0 + state_row(a, at[i]) + c, r);
-      if (packed && !(m.inside >> i & 1u)) {
-        if (!a.fill) continue;
-        vx = vg = all4(0.f);
+      for (int i = 0; i < kRun; ++i) {
+        const F4 delta = add4(d[i], r);
+        r = mul4(al[i], delta);
+        store4(px, kComp ? mul4(delta, keep[kComp ? i : 0]) : delta);
+        store4(pg, mul4(r, pull[i]));
+        px += step;
+        pg += step;
       }
-      store4(dx + (int64_t)at[i] * a.C, vx);
-      store4(dgate + (int64_t)at[i] * a.C, vg);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (i >= n) break;
+        const int64_t row = rows.next(g);
+        const F4 delta = m.last >> i & 1u ? d[i] : add4(d[i], r);
+        r = mul4(al[i], delta);
+        if (packed && a.dh0 && (m.first >> i & 1u)) store4(a.dh0 + state_row(a, (int)row) + c, r);
+        F4 vx = kComp ? mul4(delta, keep[kComp ? i : 0]) : delta, vg = mul4(r, pull[i]);
+        if (packed && !(m.inside >> i & 1u)) {
+          if (!a.fill) continue;
+          vx = vg = all4(0.f);
+        }
+        store4(dx + row * a.C, vx);
+        store4(dgate + row * a.C, vg);
+      }
     }
   }
   cp_async_wait_all();
@@ -138,10 +184,10 @@ struct Backward {
     const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
     const size_t smem = (size_t)kRun * kThreads *
                         ((kComp ? 3 : 2) * sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
-    const int64_t wide = (int64_t)a.B * ((a.C + 63) / 64);
-    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 16 * kRun)
-      return enqueue(glr_bwd_k<T, kKind, kComp, 16, kRun>, a, g, 16, kRun, 296, smem, st);
-    return enqueue(glr_bwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 296, smem, st);
+    const int64_t wide = (int64_t)a.B * ((a.C + 31) / 32);
+    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 8 * kRun)
+      return enqueue(glr_bwd_k<T, kKind, kComp, 8, kRun>, a, g, 8, kRun, 592, smem, st);
+    return enqueue(glr_bwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 592, smem, st);
   }
 };
 

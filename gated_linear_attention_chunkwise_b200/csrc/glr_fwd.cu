@@ -7,7 +7,7 @@ namespace glr {
 namespace {
 
 template <typename T, int kKind, bool kComp, int kLanes, int kRun>
-__global__ void __launch_bounds__(kThreads, 2) glr_fwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
+__global__ void __launch_bounds__(kThreads, 4) glr_fwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
   using G = GateT<T, kKind>;
   using RawT = typename Four<T>::Raw;
   using RawG = typename Four<G>::Raw;
@@ -31,15 +31,31 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_k(GlrArgs a, ScanGeom g, 
   Walk<kLanes> walk(sm, start);
   const int per_round = (int)walk.size * (kThreads / kLanes) * kRun;
   int p0 = ((int)walk.rank * (kThreads / kLanes) + threadIdx.x / kLanes) * kRun;
-  int row[kRun];
+  const uint32_t slot_g = smem_u32(sg), slot_x = smem_u32(sx);
+  constexpr uint32_t kStepG = kThreads * sizeof(RawG), kStepX = kThreads * sizeof(RawT);
   auto load = [&](int from) {
     Rows rows(g, from, 1);
+    int apart;
+    if (on && from + kRun <= g.T && rows.even(g, kRun, apart)) {
+      const int row = rows.next(g);
+      const G* pg = gate + row * a.gate_stride;
+      const T* px = x + row * a.x_stride;
+      const int64_t dg = apart * a.gate_stride, dx = apart * a.x_stride;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      const bool there = on && from + i < g.T;
-      row[i] = there ? rows.next() : 0;
-      fetch<G>(smem_u32(sg + i * kThreads), gate + row[i] * a.gate_stride, there);
-      fetch<T>(smem_u32(sx + i * kThreads), x + row[i] * a.x_stride, there);
+      for (int i = 0; i < kRun; ++i) {
+        fetch<G>(slot_g + i * kStepG, pg, true);
+        fetch<T>(slot_x + i * kStepX, px, true);
+        pg += dg;
+        px += dx;
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kRun; ++i) {
+        const bool there = on && from + i < g.T;
+        const int row = there ? rows.next(g) : 0;
+        fetch<G>(slot_g + i * kStepG, gate + row * a.gate_stride, there);
+        fetch<T>(slot_x + i * kStepX, x + row * a.x_stride, there);
+      }
     }
     cp_async_commit();
   };
@@ -49,54 +65,72 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_k(GlrArgs a, ScanGeom g, 
   cluster_wait();
 
   bool grown = false;
+  Amid amid;
   for (int round = 0; round < rounds; ++round, p0 += per_round) {
     const int n = on ? max(0, min(kRun, g.T - p0)) : 0;
     Marks m{0u, 0u, 0u};
-    if (packed) m = mark(a, a.dir ? g.T - p0 - n : p0, n, a.dir != 0);
+    if (packed) m = mark(a, a.dir ? g.T - p0 - n : p0, n, a.dir != 0, amid);
     cp_async_wait_all();
     F4 al[kRun], u[kRun];
-    Span s{all4(1.f), all4(0.f)};
+    Span s = nothing();
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
       u[i] = Four<T>::get(sx[i * kThreads]);
       if constexpr (kComp) u[i] = mul4(k.rest, u[i]);
       al[i] = k.alpha;
-      if (i >= n) {
-        al[i] = all4(1.f);
-        u[i] = all4(0.f);
-      }
-      if (m.first >> i & 1u) {
-        if (a.h0) u[i] = fma4(al[i], load4(a.h0 + state_row(a, row[i]) + c), u[i]);
-        s = Span{all4(1.f), u[i]};
-      } else {
-        s = Span{mul4(s.A, al[i]), fma4(al[i], s.h, u[i])};
-      }
+      s = i == 0 ? Span{al[0], u[0]} : Span{mul4(s.A, al[i]), fma4(al[i], s.h, u[i])};
     }
-    if (any_over(s.A) || s.A.a.x != s.A.a.x || s.A.a.y != s.A.a.y || s.A.b.x != s.A.b.x || s.A.b.y != s.A.b.y) {
-      s.A = all4(1.f);  // growth, or a NaN: multiply again with a cap
+    // Tokens that are missing or begin a sequence, growth, and NaN gates are folded again.
+    const bool plain = n == kRun && m.first == 0u;
+    bool odd = !all_within(s.A, 1.f);
+    if (!plain || odd) {
+      s = nothing();
+      Rows rows(g, p0, 1);
 #pragma unroll
-      for (int i = 0; i < kRun; ++i)
-        s.A = m.first >> i & 1u ? all4(1.f) : product<false>(s.A, cap(al[i]), grown), grown |= any_over(al[i]);
+      for (int i = 0; i < kRun; ++i) {
+        if (i >= n) {
+          al[i] = all4(1.f);
+          u[i] = all4(0.f);
+        }
+        const int row = i < n ? rows.next(g) : 0;
+        if (m.first >> i & 1u) {
+          if (a.h0) u[i] = fma4(al[i], load4(a.h0 + state_row(a, row) + c), u[i]);
+          s = Span{all4(1.f), u[i]};
+        } else {
+          s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), fma4(al[i], s.h, u[i])};
+        }
+      }
+      odd = m.first != 0u || !all_within(s.A, 1.f);
+      if (m.first) s.A.a.x = -0.f;
     }
-    if (m.first) s.A = all4(-0.f);
-    // The tokens are in registers: the slots are free for the next round's.
-    int at[kRun];
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) at[i] = row[i];
+    // The tokens are in registers: their slots are free for the next round's.
     if (round + 1 < rounds) load(p0 + per_round);
     F4 h;
-    if (!(packed ? walk.template exchange<true>(s, round, h, grown) : walk.template exchange<false>(s, round, h, grown)))
-      break;
+    if (!walk.exchange(s, odd, packed, round, h, grown)) break;
+    Rows rows(g, p0, 1);
+    int apart;
+    if (plain && m.last == 0u && rows.even(g, kRun, apart) && (!packed || m.inside == (1u << kRun) - 1u)) {
+      T* po = out + (int64_t)rows.next(g) * a.C;
+      const int64_t d = (int64_t)apart * a.C;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      h = m.first >> i & 1u ? u[i] : fma4(al[i], h, u[i]);
-      if (i >= n) continue;
-      if (!packed || (m.inside >> i & 1u))
-        store4(out + (int64_t)at[i] * a.C, h);
-      else if (a.fill)
-        store4(out + (int64_t)at[i] * a.C, all4(0.f));
-      if (a.h_last && (m.last >> i & 1u)) store4(a.h_last + state_row(a, at[i]) + c, h);
+      for (int i = 0; i < kRun; ++i) {
+        h = fma4(al[i], h, u[i]);
+        store4(po, h);
+        po += d;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (i >= n) break;
+        const int row = rows.next(g);
+        h = m.first >> i & 1u ? u[i] : fma4(al[i], h, u[i]);
+        if (!packed || (m.inside >> i & 1u))
+          store4(out + (int64_t)row * a.C, h);
+        else if (a.fill)
+          store4(out + (int64_t)row * a.C, all4(0.f));
+        if (a.h_last && (m.last >> i & 1u)) store4(a.h_last + state_row(a, row) + c, h);
+      }
     }
   }
   cp_async_wait_all();
@@ -112,10 +146,10 @@ struct Forward {
     constexpr int kRun = 8;
     const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
     const size_t smem = (size_t)kRun * kThreads * (sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
-    const int64_t wide = (int64_t)a.B * ((a.C + 63) / 64);
-    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 16 * kRun)
-      return enqueue(glr_fwd_k<T, kKind, kComp, 16, kRun>, a, g, 16, kRun, 296, smem, st);
-    return enqueue(glr_fwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 296, smem, st);
+    const int64_t wide = (int64_t)a.B * ((a.C + 31) / 32);
+    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 8 * kRun)
+      return enqueue(glr_fwd_k<T, kKind, kComp, 8, kRun>, a, g, 8, kRun, 592, smem, st);
+    return enqueue(glr_fwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 592, smem, st);
   }
 };
 

@@ -25,7 +25,7 @@
 namespace dig {
 namespace glr {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
 
@@ -33,50 +33,38 @@ constexpr int kMaxCluster = 8;
 struct Span {
   F4 A, h;
 };
-constexpr uint32_t kForget = 0x80000000u;  // sign bit of A: nothing that enters matters
+__device__ __forceinline__ Span nothing() { return Span{all4(1.f), all4(0.f)}; }
 
-__device__ __forceinline__ bool forgets(float A) { return (int)__float_as_uint(A) < 0; }
-__device__ __forceinline__ bool any_over(F4 v) {  // (a NaN compares false)
-  return v.a.x > FLT_MAX || v.a.y > FLT_MAX || v.b.x > FLT_MAX || v.b.y > FLT_MAX;
+// A span that begins a sequence forgets what enters it: the sign bit of its first A (gates
+// are never negative).
+constexpr uint32_t kForget = 0x80000000u;
+__device__ __forceinline__ bool forgets(const Span& s) { return (int)__float_as_uint(s.A.a.x) < 0; }
+
+__device__ __forceinline__ F4 enter(const Span& s, F4 in) { return fma4(s.A, in, s.h); }
+__device__ __forceinline__ F4 enter_marked(const Span& s, F4 in) { return forgets(s) ? s.h : enter(s, in); }
+__device__ __forceinline__ Span join(const Span& first, const Span& then) {
+  return Span{mul4(first.A, then.A), enter(then, first.h)};
 }
-__device__ __forceinline__ F4 cap(F4 v) {
+
+__device__ __forceinline__ bool any_over(F4 v, float most) {  // (a NaN compares false)
+  return v.a.x > most || v.a.y > most || v.b.x > most || v.b.y > most;
+}
+__device__ __forceinline__ bool all_within(F4 v, float most) {  // (a NaN compares false)
+  return v.a.x <= most && v.a.y <= most && v.b.x <= most && v.b.y <= most;
+}
+// Growth is held at the largest fp32 number (and reported), so that a zero that enters
+// later gives zero instead of NaN.
+__device__ __forceinline__ F4 capped(F4 v, bool& grown) {
+  grown |= any_over(v, FLT_MAX);
   auto c = [](float x) { return x > FLT_MAX ? FLT_MAX : x; };
   return F4{make_float2(c(v.a.x), c(v.a.y)), make_float2(c(v.b.x), c(v.b.y))};
 }
-
-// kMarks: spans may be marked to forget (packed rows).
-template <bool kMarks>
-__device__ __forceinline__ F4 enter(const Span& s, F4 in) {
-  F4 v = fma4(s.A, in, s.h);
-  if constexpr (kMarks) {
-    v.a.x = forgets(s.A.a.x) ? s.h.a.x : v.a.x;
-    v.a.y = forgets(s.A.a.y) ? s.h.a.y : v.a.y;
-    v.b.x = forgets(s.A.b.x) ? s.h.b.x : v.b.x;
-    v.b.y = forgets(s.A.b.y) ? s.h.b.y : v.b.y;
-  }
-  return v;
-}
-// A product of gates; a mark in either factor stays.  Growth is held at the largest fp32
-// number (and reported), so that a zero that enters later gives zero instead of NaN.
-template <bool kMarks>
-__device__ __forceinline__ F4 product(F4 x, F4 y, bool& grown) {
-  F4 v = mul4(x, y);
-  if (any_over(v)) {
-    grown = true;
-    v = cap(v);
-  }
-  if constexpr (kMarks) {
-    auto m = [](float r, float p, float q) {
-      return __uint_as_float(__float_as_uint(r) | ((__float_as_uint(p) | __float_as_uint(q)) & kForget));
-    };
-    v = F4{make_float2(m(v.a.x, x.a.x, y.a.x), m(v.a.y, x.a.y, y.a.y)),
-           make_float2(m(v.b.x, x.b.x, y.b.x), m(v.b.y, x.b.y, y.b.y))};
-  }
-  return v;
-}
-template <bool kMarks>
-__device__ __forceinline__ Span join(const Span& first, const Span& then, bool& grown) {
-  return Span{product<kMarks>(first.A, then.A, grown), enter<kMarks>(then, first.h)};
+// join() where a span may be marked or may grow: a mark in either stays.
+__device__ __forceinline__ Span join_marked(const Span& first, const Span& then, bool& grown) {
+  Span r{capped(mul4(first.A, then.A), grown), enter_marked(then, first.h)};
+  r.A.a.x = __uint_as_float((__float_as_uint(r.A.a.x) & ~kForget) |
+                            ((__float_as_uint(first.A.a.x) | __float_as_uint(then.A.a.x)) & kForget));
+  return r;
 }
 
 // ---- the exchange ---------------------------------------------------------------------------
@@ -144,44 +132,71 @@ struct Walk {
   }
 
   // The value that enters this thread's span s.  Returns false, in all threads of the block
-  // alike, when an earlier round's wait ran out.
+  // alike, when an earlier round's wait ran out.  odd: s is marked, or its A may exceed 1
+  // (without either no product of spans can overflow or must forget).
   //
   // Reuse of the buffers: a block sends its total of round k + 2 only after it has received
   // all totals of round k + 1, and a block sends that only after all its threads have passed
-  // the __syncthreads of round k + 1, behind their reads of round k.
-  template <bool kMarks>
-  __device__ __forceinline__ bool exchange(const Span& s, int round, F4& in, bool& grown) {
+  // the barrier of round k + 1, behind their reads of round k.
+  __device__ __forceinline__ bool exchange(const Span& s, bool odd, bool marks, int round, F4& in, bool& grown) {
     const int par = round & 1;
+    const int lane32 = threadIdx.x & 31;
     Span inc = s;  // inclusive scan over the warp's spans
+    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+      for (int off = kLanes; off < 32; off *= 2) {
+        const Span o = shift(inc, off);
+        if (lane32 >= off) inc = join_marked(o, inc, grown);
+      }
+    } else {
 #pragma unroll
-    for (int off = kLanes; off < 32; off *= 2) {
-      const Span o = shift(inc, off);
-      if ((int)(threadIdx.x & 31) >= off) inc = join<kMarks>(o, inc, grown);
-    }
-    const Span ex = shift(inc, kLanes);
-    if ((threadIdx.x & 31) >= 32 - kLanes) sm.warp[par][warp][lane] = inc;
-    if (threadIdx.x == 0) expect_bytes(smem_u32(&sm.bar[par]), size * kLanes * (uint32_t)sizeof(Span));
-    if (__syncthreads_or(late)) return false;
-    Span pre{all4(1.f), all4(0.f)};  // the warps before this one
-    for (int i = 0; i < warp; ++i) pre = i == 0 ? sm.warp[par][0][lane] : join<kMarks>(pre, sm.warp[par][i][lane], grown);
-    if (warp == kWarps - 1 && seg == 32 / kLanes - 1) {
-      const Span t = join<kMarks>(pre, inc, grown);
-      const uint32_t to = smem_u32(&sm.total[par][rank][lane]), bar = smem_u32(&sm.bar[par]);
-      for (uint32_t r = 0; r < size; ++r) {
-        const uint32_t addr = map_to(to, r), at = map_to(bar, r);
-        store_async(addr, at, t.A);
-        store_async(addr + 16u, at, t.h);
+      for (int off = kLanes; off < 32; off *= 2) {
+        const Span o = shift(inc, off);
+        if (lane32 >= off) inc = join(o, inc);
       }
     }
-    if (seg) pre = join<kMarks>(pre, ex, grown);
+    Span pre = shift(inc, kLanes);
+    if (seg == 0) pre = nothing();
+    if (seg == 32 / kLanes - 1) sm.warp[par][warp][lane] = inc;
+    if (threadIdx.x == 0) expect_bytes(smem_u32(&sm.bar[par]), size * kLanes * (uint32_t)sizeof(Span));
+    const bool special = __syncthreads_or(odd || late);
+    if (special && __syncthreads_or(late)) return false;
+    Span all = nothing();  // the warps before this one, then the whole block
+    if (special) {
+#pragma unroll 1
+      for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) pre = join_marked(all, pre, grown);
+        all = join_marked(all, sm.warp[par][i][lane], grown);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWarps; ++i) {
+        if (i == warp) pre = join(all, pre);
+        all = join(all, sm.warp[par][i][lane]);
+      }
+    }
+    // Thread r * kLanes + lane sends the block's total to block r.
+    if (threadIdx.x < size * kLanes) {
+      const uint32_t r = threadIdx.x / kLanes;
+      const uint32_t to = map_to(smem_u32(&sm.total[par][rank][lane]), r), at = map_to(smem_u32(&sm.bar[par]), r);
+      store_async(to, at, all.A);
+      store_async(to + 16u, at, all.h);
+    }
     if (!mbar_wait(smem_u32(&sm.bar[par]), (round >> 1) & 1)) {
       report_status(GLA_ERR_TIMEOUT);
       late = true;
     }
     F4 v = carry;
-    for (uint32_t r = 0; r < size; ++r) {
-      if (r == rank) in = enter<kMarks>(pre, v);
-      v = enter<kMarks>(sm.total[par][r][lane], v);
+    if (marks) {
+      for (uint32_t r = 0; r < size; ++r) {
+        if (r == rank) in = enter_marked(pre, v);
+        v = enter_marked(sm.total[par][r][lane], v);
+      }
+    } else {
+      for (uint32_t r = 0; r < size; ++r) {
+        if (r == rank) in = enter(pre, v);
+        v = enter(sm.total[par][r][lane], v);
+      }
     }
     carry = v;
     return true;
@@ -203,21 +218,28 @@ struct Walk {
 
 // ---- tokens -----------------------------------------------------------------------------------
 
-// Rows of scan positions p, p + step, ... (step +-1): one division, then increments.
+// Rows of scan positions p, p + step, ... (step +-1), and whether the first `count` of
+// them are evenly spaced in memory (`apart` rows).
 struct Rows {
-  const ScanGeom& g;
-  int p, step, f, x, y, df;
+  int f, df, x, y, p, step;
 
-  __device__ __forceinline__ Rows(const ScanGeom& geom, int first, int by) : g(geom), p(first), step(by) {
+  __device__ __forceinline__ Rows(const ScanGeom& g, int first, int by) : p(first), step(by) {
     f = g.reverse ? g.T - 1 - p : p;  // position in the base order
     df = g.reverse ? -step : step;
+    x = y = 0;
     if (g.column_base) {
       x = f / g.Hg;  // (a position before the first token is never used)
       y = f - x * g.Hg;
     }
   }
-  __device__ __forceinline__ int next() {
-    int row;
+  __device__ __forceinline__ bool even(const ScanGeom& g, int count, int& apart) const {
+    apart = g.column_base ? df * g.Wg : df;
+    if (g.zigzag) return false;
+    const int last = y + df * (count - 1);
+    return !g.column_base || (last >= 0 && last < g.Hg);
+  }
+  __device__ __forceinline__ int next(const ScanGeom& g) {
+    int row = f;
     if (g.zigzag) {
       row = zigzag_token(g, p);
     } else if (g.column_base) {
@@ -230,8 +252,6 @@ struct Rows {
         y = g.Hg - 1;
         --x;
       }
-    } else {
-      row = f;
     }
     f += df;
     p += step;
@@ -274,15 +294,20 @@ __device__ __forceinline__ int64_t state_row(const GlrArgs& a, int t) {
 struct Marks {
   uint32_t inside, first, last;
 };
+// The sequence a thread was last amid: tokens strictly between its ends need no search.
+struct Amid {
+  int begin = 0, end = 0;
+};
 // The tokens are lo .. lo + n - 1; turned: walked from the highest to the lowest.
-__device__ __forceinline__ Marks mark(const GlrArgs& a, int lo, int n, bool turned) {
-  Marks m{0u, 0u, 0u};
-  if (n <= 0) return m;
+__device__ __forceinline__ Marks mark(const GlrArgs& a, int lo, int n, bool turned, Amid& at) {
+  Marks m{(1u << n) - 1u, 0u, 0u};
+  if (n <= 0 || (lo > at.begin && lo + n < at.end)) return m;
   int q = find_sequence(a.cu, a.nseq, lo);
-  if (q >= 0 && a.cu[q] < lo && a.cu[q + 1] > lo + n) {  // amid one sequence: the usual case
-    m.inside = (1u << n) - 1u;
-    return m;
+  if (q >= 0) {
+    at = Amid{a.cu[q], a.cu[q + 1]};
+    if (lo > at.begin && lo + n < at.end) return m;
   }
+  m.inside = 0u;
   for (int i = 0; i < n; ++i) {
     const int t = lo + i;
     while (q + 1 < a.nseq && a.cu[q + 1] <= t) ++q;

@@ -81,11 +81,19 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_k(GlrArgs a, ScanGeom g, 
 
   bool grown = false;
   Amid amid;
+  Marks next{0u, 0u, 0u};
+  F4 next_entry = all4(0.f);
+  auto look = [&](int from) {
+    // Backwards over sequences in token order the token falls by one each step.
+    const int n = on ? max(0, min(kRun, g.T - from)) : 0;
+    next = mark(a, a.dir ? from : g.T - from - n, n, a.dir == 0, amid);
+    next_entry = entering(a, a.dh_last, next.last, a.dir ? from : g.T - 1 - from, a.dir ? 1 : -1, c);
+  };
+  if (packed) look(j0);
   for (int round = 0; round < rounds; ++round, j0 += per_round) {
     const int n = on ? max(0, min(kRun, g.T - j0)) : 0;
-    // Backwards over sequences in token order the token falls by one each step.
-    Marks m{0u, 0u, 0u};
-    if (packed) m = mark(a, a.dir ? j0 : g.T - j0 - n, n, a.dir == 0, amid);
+    Marks m = next;
+    const F4 entry = next_entry;
     if (!packed && n > 0 && j0 + n == g.T) m.first = 1u << (n - 1);  // the scan's first token
     cp_async_wait_all();
     // pull = (h before - [complement] x) d log_alpha / d gate, keep = 1 - alpha.
@@ -125,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_k(GlrArgs a, ScanGeom g, 
         }
         const int row = i < n ? rows.next(g) : 0;
         if (m.last >> i & 1u) {
-          if (a.dh_last) d[i] = add4(d[i], load4(a.dh_last + state_row(a, row) + c));
+          if (a.dh_last)
+            d[i] = add4(d[i], m.last & ((1u << i) - 1u) ? load4(a.dh_last + state_row(a, row) + c) : entry);
           s = Span{all4(1.f), mul4(al[i], d[i])};
         } else {
           s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), mul4(al[i], add4(d[i], s.h))};
@@ -134,9 +143,14 @@ __global__ void __launch_bounds__(kThreads, 4) glr_bwd_k(GlrArgs a, ScanGeom g, 
       odd = m.last != 0u || !all_within(s.A, 1.f);
       if (m.last) s.A.a.x = -0.f;
     }
-    if (round + 1 < rounds) load(j0 + per_round);
     F4 r;
-    if (!walk.exchange(s, odd, packed, round, r, grown)) break;
+    const bool going = walk.exchange(s, odd, packed, round, r, grown, [&] {
+      if (round + 1 < rounds) {
+        load(j0 + per_round);
+        if (packed) look(j0 + per_round);
+      }
+    });
+    if (!going) break;
     Rows rows(g, g.T - 1 - j0, -1);
     int apart;
     if (plain && (!packed || m.first == 0u) && rows.even(g, kRun, apart) && (!packed || m.inside == (1u << kRun) - 1u)) {
@@ -185,9 +199,10 @@ struct Backward {
     const size_t smem = (size_t)kRun * kThreads *
                         ((kComp ? 3 : 2) * sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
     const int64_t wide = (int64_t)a.B * ((a.C + 31) / 32);
+    static Known known8, known4;
     if (wide * kMaxCluster >= 148 || g.T <= kThreads / 8 * kRun)
-      return enqueue(glr_bwd_k<T, kKind, kComp, 8, kRun>, a, g, 8, kRun, 592, smem, st);
-    return enqueue(glr_bwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 592, smem, st);
+      return enqueue(glr_bwd_k<T, kKind, kComp, 8, kRun>, known8, a, g, 8, kRun, smem, st);
+    return enqueue(glr_bwd_k<T, kKind, kComp, 4, kRun>, known4, a, g, 4, kRun, smem, st);
   }
 };
 

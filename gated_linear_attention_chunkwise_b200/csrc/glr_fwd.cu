@@ -66,10 +66,18 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_k(GlrArgs a, ScanGeom g, 
 
   bool grown = false;
   Amid amid;
+  Marks next{0u, 0u, 0u};
+  F4 next_entry = all4(0.f);
+  auto look = [&](int from) {
+    const int n = on ? max(0, min(kRun, g.T - from)) : 0;
+    next = mark(a, a.dir ? g.T - from - n : from, n, a.dir != 0, amid);
+    next_entry = entering(a, a.h0, next.first, a.dir ? g.T - 1 - from : from, a.dir ? -1 : 1, c);
+  };
+  if (packed) look(p0);
   for (int round = 0; round < rounds; ++round, p0 += per_round) {
     const int n = on ? max(0, min(kRun, g.T - p0)) : 0;
-    Marks m{0u, 0u, 0u};
-    if (packed) m = mark(a, a.dir ? g.T - p0 - n : p0, n, a.dir != 0, amid);
+    const Marks m = next;
+    const F4 entry = next_entry;
     cp_async_wait_all();
     F4 al[kRun], u[kRun];
     Span s = nothing();
@@ -95,7 +103,8 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_k(GlrArgs a, ScanGeom g, 
         }
         const int row = i < n ? rows.next(g) : 0;
         if (m.first >> i & 1u) {
-          if (a.h0) u[i] = fma4(al[i], load4(a.h0 + state_row(a, row) + c), u[i]);
+          if (a.h0)
+            u[i] = fma4(al[i], m.first & ((1u << i) - 1u) ? load4(a.h0 + state_row(a, row) + c) : entry, u[i]);
           s = Span{all4(1.f), u[i]};
         } else {
           s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), fma4(al[i], s.h, u[i])};
@@ -104,10 +113,15 @@ __global__ void __launch_bounds__(kThreads, 4) glr_fwd_k(GlrArgs a, ScanGeom g, 
       odd = m.first != 0u || !all_within(s.A, 1.f);
       if (m.first) s.A.a.x = -0.f;
     }
-    // The tokens are in registers: their slots are free for the next round's.
-    if (round + 1 < rounds) load(p0 + per_round);
     F4 h;
-    if (!walk.exchange(s, odd, packed, round, h, grown)) break;
+    const bool going = walk.exchange(s, odd, packed, round, h, grown, [&] {
+      // The tokens are in registers: their slots are free for the next round's.
+      if (round + 1 < rounds) {
+        load(p0 + per_round);
+        if (packed) look(p0 + per_round);
+      }
+    });
+    if (!going) break;
     Rows rows(g, p0, 1);
     int apart;
     if (plain && m.last == 0u && rows.even(g, kRun, apart) && (!packed || m.inside == (1u << kRun) - 1u)) {
@@ -147,9 +161,10 @@ struct Forward {
     const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
     const size_t smem = (size_t)kRun * kThreads * (sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
     const int64_t wide = (int64_t)a.B * ((a.C + 31) / 32);
+    static Known known8, known4;
     if (wide * kMaxCluster >= 148 || g.T <= kThreads / 8 * kRun)
-      return enqueue(glr_fwd_k<T, kKind, kComp, 8, kRun>, a, g, 8, kRun, 592, smem, st);
-    return enqueue(glr_fwd_k<T, kKind, kComp, 4, kRun>, a, g, 4, kRun, 592, smem, st);
+      return enqueue(glr_fwd_k<T, kKind, kComp, 8, kRun>, known8, a, g, 8, kRun, smem, st);
+    return enqueue(glr_fwd_k<T, kKind, kComp, 4, kRun>, known4, a, g, 4, kRun, smem, st);
   }
 };
 

@@ -20,6 +20,9 @@
 // fold then selects instead of multiplying by zero, so a NaN ends with its sequence.
 #pragma once
 
+#include <algorithm>
+#include <atomic>
+
 #include "glr.cuh"
 
 namespace dig {
@@ -138,7 +141,11 @@ struct Walk {
   // Reuse of the buffers: a block sends its total of round k + 2 only after it has received
   // all totals of round k + 1, and a block sends that only after all its threads have passed
   // the barrier of round k + 1, behind their reads of round k.
-  __device__ __forceinline__ bool exchange(const Span& s, bool odd, bool marks, int round, F4& in, bool& grown) {
+  //
+  // meanwhile() runs while the totals travel: the next round's copies and searches.
+  template <typename F>
+  __device__ __forceinline__ bool exchange(const Span& s, bool odd, bool marks, int round, F4& in, bool& grown,
+                                           F meanwhile) {
     const int par = round & 1;
     const int lane32 = threadIdx.x & 31;
     Span inc = s;  // inclusive scan over the warp's spans
@@ -182,6 +189,7 @@ struct Walk {
       store_async(to, at, all.A);
       store_async(to + 16u, at, all.h);
     }
+    meanwhile();
     if (!mbar_wait(smem_u32(&sm.bar[par]), (round >> 1) & 1)) {
       report_status(GLA_ERR_TIMEOUT);
       late = true;
@@ -289,6 +297,13 @@ __device__ __forceinline__ int64_t state_row(const GlrArgs& a, int t) {
   return (int64_t)max(find_sequence(a.cu, a.nseq, t), 0) * a.C;
 }
 
+// The state h0 or dh_last that enters at the first marked token, fetched a round ahead: a
+// thread that waited for it would hold up its whole cluster.
+__device__ __forceinline__ F4 entering(const GlrArgs& a, const float* states, uint32_t marks, int token0, int by, int c) {
+  if (!states || marks == 0u) return all4(0.f);
+  return load4(states + state_row(a, token0 + by * (__ffs(marks) - 1)) + c);
+}
+
 // Of a thread's tokens (bit i: the i-th it walks): which lie in a sequence, begin one, end
 // one (first and last in scan order).
 struct Marks {
@@ -336,18 +351,42 @@ __device__ __forceinline__ void empty_sequences(const GlrArgs& a, int T, int c0,
 // ---- launch -------------------------------------------------------------------------------------
 using Kernel = void (*)(GlrArgs, ScanGeom, int, int);
 
-// The widest cluster, up to 8, for which all blocks find room (`room` of them) and have tokens.
-inline int cluster_for(int64_t slabs, int T, int per_block, int64_t room) {
-  int c = 1;
-  while (c < kMaxCluster && slabs * c * 2 <= room && (int64_t)c * per_block < T) c *= 2;
-  return c;
+// How many clusters of `size` blocks run at once on the current device.
+inline int resident_clusters(Kernel k, int size, size_t smem, std::atomic<int>* known) {
+  int n = known[size].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = size;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.gridDim = dim3(size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();
+    return 1;
+  }
+  known[size].store(n, std::memory_order_relaxed);
+  return n;
 }
 
-inline cudaError_t enqueue(Kernel k, const GlrArgs& a, const ScanGeom& g, int lanes, int run, int room, size_t smem,
+// `known`: a table of the kernel's own, [device][cluster size], for the figures above.
+using Known = std::atomic<int>[64][kMaxCluster + 1];
+
+inline cudaError_t enqueue(Kernel k, Known& known, const GlrArgs& a, const ScanGeom& g, int lanes, int run, size_t smem,
                            cudaStream_t st) {
   const int slabs = (a.C + 4 * lanes - 1) / (4 * lanes);
   const int per_block = kThreads / lanes * run;
-  const int cluster = cluster_for((int64_t)a.B * slabs, g.T, per_block, room);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  // The widest cluster that has tokens for all its blocks and whose copies, one a slab, all
+  // run at once (a second wave of a few clusters would double the time).
+  int cluster = (int)std::min<int64_t>(kMaxCluster, ((int64_t)g.T + per_block - 1) / per_block);
+  while (cluster > 1 && (int64_t)a.B * slabs > resident_clusters(k, cluster, smem, known[dev & 63])) --cluster;
   const int64_t per_round = (int64_t)cluster * per_block;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
@@ -360,8 +399,6 @@ inline cudaError_t enqueue(Kernel k, const GlrArgs& a, const ScanGeom& g, int la
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, k, a, g, slabs, (int)((g.T + per_round - 1) / per_round));
 }
 

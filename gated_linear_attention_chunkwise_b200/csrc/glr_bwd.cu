@@ -8,7 +8,7 @@ namespace glr {
 namespace {
 
 template <typename T, int kKind, bool kComp, int kLanes, int kRun>
-__global__ void __launch_bounds__(kThreads, 4) glr_bwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
+__global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
   using G = GateT<T, kKind>;
   using RawT = typename Four<T>::Raw;
   using RawG = typename Four<G>::Raw;

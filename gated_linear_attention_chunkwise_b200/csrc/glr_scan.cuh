@@ -108,6 +108,7 @@ template <int kLanes>
 struct Shared {
   Span warp[2][kWarps][kLanes];        // spans of this block's warps, by parity of the round
   Span total[2][kMaxCluster][kLanes];  // spans of the cluster's blocks
+  F4 entry[kLanes];                    // what enters this block
   uint64_t bar[2];                     // total[i] has arrived
 };
 
@@ -117,8 +118,7 @@ struct Walk {
   Shared<kLanes>& sm;
   uint32_t rank, size;
   int lane, warp, seg;  // channel group in the slab; warp; the thread's span within the warp
-  F4 carry;             // the value at the start of the round
-  bool late = false;    // a wait ran out
+  F4 carry;             // the value at the start of the round (kept by the first warp)
 
   __device__ __forceinline__ Walk(Shared<kLanes>& s, const F4& start) : sm(s), carry(start) {
     rank = cluster_rank();
@@ -135,14 +135,14 @@ struct Walk {
   }
 
   // The value that enters this thread's span s.  Returns false, in all threads of the block
-  // alike, when an earlier round's wait ran out.  odd: s is marked, or its A may exceed 1
-  // (without either no product of spans can overflow or must forget).
+  // alike, when the wait for the other blocks ran out.  odd: s is marked, or its A may exceed
+  // 1 (without either no product of spans can overflow or must forget).  marks: spans of the
+  // slab may be marked.  meanwhile() runs while the totals travel: the next round's copies
+  // and searches.
   //
   // Reuse of the buffers: a block sends its total of round k + 2 only after it has received
   // all totals of round k + 1, and a block sends that only after all its threads have passed
   // the barrier of round k + 1, behind their reads of round k.
-  //
-  // meanwhile() runs while the totals travel: the next round's copies and searches.
   template <typename F>
   __device__ __forceinline__ bool exchange(const Span& s, bool odd, bool marks, int round, F4& in, bool& grown,
                                            F meanwhile) {
@@ -166,47 +166,51 @@ struct Walk {
     if (seg == 0) pre = nothing();
     if (seg == 32 / kLanes - 1) sm.warp[par][warp][lane] = inc;
     if (threadIdx.x == 0) expect_bytes(smem_u32(&sm.bar[par]), size * kLanes * (uint32_t)sizeof(Span));
-    const bool special = __syncthreads_or(odd || late);
-    if (special && __syncthreads_or(late)) return false;
-    Span all = nothing();  // the warps before this one, then the whole block
+    const bool special = __syncthreads_or(odd);
+    Span before = nothing();  // the warps before this one
+    Span all;                 // the block
     if (special) {
 #pragma unroll 1
-      for (int i = 0; i < kWarps; ++i) {
-        if (i == warp) pre = join_marked(all, pre, grown);
-        all = join_marked(all, sm.warp[par][i][lane], grown);
-      }
+      for (int i = 0; i < warp; ++i) before = join_marked(before, sm.warp[par][i][lane], grown);
+      pre = join_marked(before, pre, grown);
+      if (warp == kWarps - 1) all = join_marked(before, sm.warp[par][warp][lane], grown);
     } else {
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) {
-        if (i == warp) pre = join(all, pre);
-        all = join(all, sm.warp[par][i][lane]);
-      }
+      for (int i = 0; i < warp; ++i) before = join(before, sm.warp[par][i][lane]);
+      pre = join(before, pre);
+      if (warp == kWarps - 1) all = join(before, sm.warp[par][warp][lane]);
     }
-    // Thread r * kLanes + lane sends the block's total to block r.
-    if (threadIdx.x < size * kLanes) {
-      const uint32_t r = threadIdx.x / kLanes;
-      const uint32_t to = map_to(smem_u32(&sm.total[par][rank][lane]), r), at = map_to(smem_u32(&sm.bar[par]), r);
-      store_async(to, at, all.A);
-      store_async(to + 16u, at, all.h);
+    if (warp == kWarps - 1) {
+      const uint32_t to = smem_u32(&sm.total[par][rank][lane]), bar = smem_u32(&sm.bar[par]);
+      for (uint32_t r = seg; r < size; r += 32 / kLanes) {
+        const uint32_t addr = map_to(to, r), at = map_to(bar, r);
+        store_async(addr, at, all.A);
+        store_async(addr + 16u, at, all.h);
+      }
     }
     meanwhile();
-    if (!mbar_wait(smem_u32(&sm.bar[par]), (round >> 1) & 1)) {
-      report_status(GLA_ERR_TIMEOUT);
-      late = true;
-    }
-    F4 v = carry;
-    if (marks) {
-      for (uint32_t r = 0; r < size; ++r) {
-        if (r == rank) in = enter_marked(pre, v);
-        v = enter_marked(sm.total[par][r][lane], v);
+    bool late = false;
+    if (warp == 0) {
+      if (!mbar_wait(smem_u32(&sm.bar[par]), (round >> 1) & 1)) {
+        report_status(GLA_ERR_TIMEOUT);
+        late = true;
       }
-    } else {
-      for (uint32_t r = 0; r < size; ++r) {
-        if (r == rank) in = enter(pre, v);
-        v = enter(sm.total[par][r][lane], v);
+      F4 v = carry, mine = carry;
+      if (marks) {
+        for (uint32_t r = 0; r < size; ++r) {
+          v = enter_marked(sm.total[par][r][lane], v);
+          if (r + 1 == rank) mine = v;
+        }
+      } else {
+        for (uint32_t r = 0; r < size; ++r) {
+          v = enter(sm.total[par][r][lane], v);
+          if (r + 1 == rank) mine = v;
+        }
       }
+      carry = v;
+      if (seg == 0) sm.entry[lane] = mine;
     }
-    carry = v;
+    if (__syncthreads_or(late)) return false;
+    in = marks ? enter_marked(pre, sm.entry[lane]) : enter(pre, sm.entry[lane]);
     return true;
   }
 
@@ -373,7 +377,8 @@ inline int resident_clusters(Kernel k, int size, size_t smem, std::atomic<int>* 
   return n;
 }
 
-// `known`: a table of the kernel's own, [device][cluster size], for the figures above.
+// `known`: a table of the kernel's own, [device][cluster size], for the figures above; [device][0]:
+// its shared memory is set up.
 using Known = std::atomic<int>[64][kMaxCluster + 1];
 
 inline cudaError_t enqueue(Kernel k, Known& known, const GlrArgs& a, const ScanGeom& g, int lanes, int run, size_t smem,
@@ -383,6 +388,10 @@ inline cudaError_t enqueue(Kernel k, Known& known, const GlrArgs& a, const ScanG
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (known[dev & 63][0].load(std::memory_order_relaxed) == 0) {
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    known[dev & 63][0].store(1, std::memory_order_relaxed);
+  }
   // The widest cluster that has tokens for all its blocks and whose copies, one a slab, all
   // run at once (a second wave of a few clusters would double the time).
   int cluster = (int)std::min<int64_t>(kMaxCluster, ((int64_t)g.T + per_block - 1) / per_block);

@@ -1,165 +1,401 @@
 // qk_rope.cu -- rotary positions of query and key heads, alone or behind an RMS norm of
 // every head, and the gradients (include/dig_gla.h, rope, qk_norm_rope, qk_norm_rope_bwd).
+//
+// Mathematics: y = scale R(position * inv_freq) (x r w), r = 1 / sqrt(mean(x^2) + eps); the
+// gradient turns back first, g = scale R^T dy, and with n = x r:
+// dx = r (w g - n mean(w g n)), dw = sum of g n.
+//
+// Bound: memory.  Every head is read and written once (the gradient: two reads, one write).
+//
+// Split.  Eight channels that rotate among themselves are a unit: quads i and i + rot / 8
+// of the head when pairs are half a span apart, two adjacent quads when they are interleaved
+// or not rotated.  A group of lanes (a power of two, kUnits units each) holds a head in
+// registers and sums its squares by shuffles; a warp takes the heads of one token, group by
+// group, kHeads of them in flight.  The warp computes the token's angles once, one pair a
+// lane, and keeps cos and sin in shared memory.  A head of n units takes the next power
+// of two of lanes, or a quarter of that with three units a lane where n fits in three
+// quarters of it (72 channels: 9 units on 4 x 3 instead of 16 lanes).  With few tokens a
+// token's heads are shared between warps.
 #include <math.h>
 
-#include "dev_common.cuh"
+#include <algorithm>
+
+#include "four.cuh"
 #include "internal.h"
 
 namespace dig {
 
 namespace {
 
-__device__ __forceinline__ float ld(const float* p) { return *p; }
-__device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void st(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+constexpr int kThreads = 128;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxPairs = 128;
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+// ---- angles -----------------------------------------------------------------------------
 
-// cos and sin of position * inv_freq, times scale.  The angle is formed in fp64 and
-// reduced to a fraction of a turn there, so far positions keep their phase.
-__device__ __forceinline__ float2 phase(const QkRopeArgs& a, int64_t row, int pair) {
+struct Turn {
+  F4 c, s;
+};
+
+// cos and sin of position * inv_freq, times scale.  The angle is formed in fp64, in turns,
+// and reduced there to half a turn, so far positions keep their phase.
+__device__ __forceinline__ void angles(const QkRopeArgs& a, int64_t row, float2* cs) {
   double pos;
   if (!a.positions)
     pos = (double)(row % a.period);
   else
     pos = a.positions64 ? (double)static_cast<const long long*>(a.positions)[row]
                         : (double)static_cast<const int*>(a.positions)[row];
-  double turn = pos * ((double)a.inv_freq[pair] * 0.15915494309189535);
-  turn -= rint(turn);
-  float s, c;
-  sincospif(2.f * (float)turn, &s, &c);
-  return make_float2(c * a.scale, s * a.scale);
-}
-
-__device__ __forceinline__ void pair_channels(const QkRopeArgs& a, int pair, int& i, int& j) {
-  i = a.interleaved ? 2 * pair : pair;
-  j = a.interleaved ? 2 * pair + 1 : pair + a.rot / 2;
-}
-
-// One warp per (row, head).
-template <typename T>
-__global__ void __launch_bounds__(128) qk_rope_k(QkRopeArgs a) {
-  const int lane = threadIdx.x & 31, H = a.q.H + a.k.H;
-  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (item >= a.rows * H) return;
-  const int64_t row = item / H;
-  int head = (int)(item - row * H);
-  const HeadRows& t = head < a.q.H ? a.q : a.k;
-  if (head >= a.q.H) head -= a.q.H;
-  const T* in = static_cast<const T*>(t.in) + row * t.stride + (int64_t)head * a.D;
-  T* out = static_cast<T*>(t.out) + row * t.out_stride + (int64_t)head * a.D;
-  float r = 1.f;
-  if (t.weight) {
-    float ss = 0.f;
-    for (int c = lane; c < a.D; c += 32) ss = fmaf(ld(in + c), ld(in + c), ss);
-    r = rsqrtf(warp_sum(ss) / a.D + a.eps);
+  for (int p = threadIdx.x & 31; p < a.rot / 2; p += 32) {
+    double turn = pos * ((double)a.inv_freq[p] * 0.15915494309189535);
+    turn -= rint(turn);
+    float s, c;
+    sincospif(2.f * (float)turn, &s, &c);
+    cs[p] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
   }
-  auto norm = [&](int c) { return t.weight ? ld(in + c) * r * t.weight[c] : ld(in + c); };
-  for (int p = lane; p < a.rot / 2; p += 32) {
-    int i, j;
-    pair_channels(a, p, i, j);
-    float2 w = phase(a, row, p);
-    if (a.inverse) w.y = -w.y;
-    const float u = norm(i), v = norm(j);
-    st(out + i, u * w.x - v * w.y);
-    st(out + j, v * w.x + u * w.y);
-  }
-  for (int c = a.rot + lane; c < a.D; c += 32) st(out + c, norm(c));
 }
 
-constexpr int kBwdBlocks = 148;
+// Four consecutive pairs' cos and sin.
+__device__ __forceinline__ Turn turn_of(const float2* cs) {
+  const float4 p = reinterpret_cast<const float4*>(cs)[0], q = reinterpret_cast<const float4*>(cs)[1];
+  return Turn{F4{make_float2(p.x, p.z), make_float2(q.x, q.z)}, F4{make_float2(p.y, p.w), make_float2(q.y, q.w)}};
+}
 
-// The gradients: a block takes rows blockIdx.x, blockIdx.x + gridDim.x, ...; its partial
-// weight gradients go to the workspace, [2][block][D].
-template <typename T>
-__global__ void __launch_bounds__(256) qk_norm_rope_bwd_k(QkRopeArgs a, float* part) {
-  __shared__ float dy[8][256];
-  __shared__ float dw[8][2][256];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, H = a.q.H + a.k.H;
-  for (int c = lane; c < 512; c += 32) dw[w][c >> 8][c & 255] = 0.f;
+// ---- units ------------------------------------------------------------------------------
+
+// Where a lane's unit lies in a head: channels a .. a + 3 and b .. b + 3.
+struct Unit {
+  int a, b;
+  bool on, turned;
+};
+template <bool kInter>
+__device__ __forceinline__ Unit unit(const QkRopeArgs& q, int i) {
+  Unit u;
+  u.on = i < q.D / 8;
+  u.turned = i < q.rot / 8;
+  const bool halves = !kInter && u.turned;
+  u.a = halves ? 4 * i : kInter ? 8 * i : q.rot + 8 * (i - q.rot / 8);
+  u.b = halves ? 4 * i + q.rot / 2 : u.a + 4;
+  return u;
+}
+
+// The unit's channels as pairs: X holds the first of each, Y the second.
+struct Pairs {
+  F4 x, y;
+};
+template <bool kInter>
+__device__ __forceinline__ Pairs as_pairs(F4 a, F4 b) {
+  if constexpr (!kInter) return Pairs{a, b};
+  return Pairs{F4{make_float2(a.a.x, a.b.x), make_float2(b.a.x, b.b.x)}, F4{make_float2(a.a.y, a.b.y), make_float2(b.a.y, b.b.y)}};
+}
+template <bool kInter>
+__device__ __forceinline__ void as_quads(const Pairs& p, F4& a, F4& b) {
+  if constexpr (kInter) {
+    a = F4{make_float2(p.x.a.x, p.y.a.x), make_float2(p.x.a.y, p.y.a.y)};
+    b = F4{make_float2(p.x.b.x, p.y.b.x), make_float2(p.x.b.y, p.y.b.y)};
+  } else {
+    a = p.x;
+    b = p.y;
+  }
+}
+__device__ __forceinline__ Pairs rotate(const Pairs& p, const Turn& t) {
+  return Pairs{sub4(mul4(p.x, t.c), mul4(p.y, t.s)), fma4(p.y, t.c, mul4(p.x, t.s))};
+}
+__device__ __forceinline__ Pairs rotate_back(const Pairs& p, const Turn& t) {
+  return Pairs{fma4(p.x, t.c, mul4(p.y, t.s)), sub4(mul4(p.y, t.c), mul4(p.x, t.s))};
+}
+__device__ __forceinline__ Pairs times(const Pairs& p, const Pairs& q) { return Pairs{mul4(p.x, q.x), mul4(p.y, q.y)}; }
+__device__ __forceinline__ Pairs scaled(const Pairs& p, float f) { return Pairs{mul4(p.x, all4(f)), mul4(p.y, all4(f))}; }
+__device__ __forceinline__ F4 dot4(const Pairs& p, const Pairs& q, F4 sum) { return fma4(p.y, q.y, fma4(p.x, q.x, sum)); }
+__device__ __forceinline__ float sum4(F4 v) {
+  const float2 s = __fadd2_rn(v.a, v.b);
+  return s.x + s.y;
+}
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  for (int o = lanes >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// How a warp's lanes and the launch's warps share the work.
+struct Split {
+  int lanes;       // lanes a head takes
+  int q_steps, k_steps;  // passes of a warp's groups over a token's heads
+  int parts;       // warps that share a token
+  int64_t items;   // rows * parts
+};
+
+// ---- forward ------------------------------------------------------------------------------
+template <typename T, bool kNorm, bool kInter, int kUnits, int kHeads>
+__global__ void __launch_bounds__(kThreads) qk_rope_k(QkRopeArgs a, Split w) {
+  using Raw = typename Four<T>::Raw;
+  __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
+  if (item >= w.items) return;
+  const int64_t row = w.parts == 1 ? item : item / w.parts;
+  const int part = (int)(item - row * w.parts);
+  const int group = lane / w.lanes, groups = 32 / w.lanes, within = lane & (w.lanes - 1);
+  Unit at[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) at[u] = unit<kInter>(a, u * w.lanes + within);
+  angles(a, row, cs[warp]);
   __syncwarp();
-  for (int64_t item = (int64_t)blockIdx.x * 8 + w; item < a.rows * H; item += (int64_t)gridDim.x * 8) {
-    const int64_t row = item / H;
-    int head = (int)(item - row * H);
-    const int which = head < a.q.H ? 0 : 1;
+  Turn turn[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u)
+    if (at[u].turned) turn[u] = turn_of(cs[warp] + 4 * (u * w.lanes + within));
+
+  const int steps = w.q_steps + w.k_steps;
+  const int first = (int)((int64_t)steps * part / w.parts), last = (int)((int64_t)steps * (part + 1) / w.parts);
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
     const HeadRows& t = which ? a.k : a.q;
-    if (which) head -= a.q.H;
-    const T* in = static_cast<const T*>(t.in) + row * t.stride + (int64_t)head * a.D;
-    const T* g = static_cast<const T*>(t.grad) + row * t.grad_stride + (int64_t)head * a.D;
-    T* out = static_cast<T*>(t.out) + row * t.out_stride + (int64_t)head * a.D;
-    for (int p = lane; p < a.rot / 2; p += 32) {
-      int i, j;
-      pair_channels(a, p, i, j);
-      const float2 f = phase(a, row, p);
-      const float u = ld(g + i), v = ld(g + j);
-      dy[w][i] = u * f.x + v * f.y;
-      dy[w][j] = v * f.x - u * f.y;
+    const int from = which ? max(first - w.q_steps, 0) : first, to = which ? last - w.q_steps : min(last, w.q_steps);
+    if (from >= to) continue;
+    const T* in = static_cast<const T*>(t.in) + row * t.stride;
+    T* out = static_cast<T*>(t.out) + row * t.out_stride;
+    Pairs weight[kUnits];
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (at[u].on) weight[u] = as_pairs<kInter>(load4(t.weight + at[u].a), load4(t.weight + at[u].b));
     }
-    for (int c = a.rot + lane; c < a.D; c += 32) dy[w][c] = ld(g + c);
+#pragma unroll 1
+    for (int step = from; step < to; step += kHeads) {
+      Raw ra[kHeads][kUnits], rb[kHeads][kUnits];
+      bool there[kHeads];
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k) {
+        const int head = (step + k) * groups + group;
+        there[k] = step + k < to && head < t.H;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          ra[k][u] = rb[k][u] = Raw{};
+          if (there[k] && at[u].on) {
+            ra[k][u] = *reinterpret_cast<const Raw*>(in + head * a.D + at[u].a);
+            rb[k][u] = *reinterpret_cast<const Raw*>(in + head * a.D + at[u].b);
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kHeads; ++k) {
+        T* to_head = out + ((step + k) * groups + group) * a.D;
+        Pairs p[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) p[u] = as_pairs<kInter>(Four<T>::get(ra[k][u]), Four<T>::get(rb[k][u]));
+        if constexpr (kNorm) {
+          F4 ss = all4(0.f);
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) ss = dot4(p[u], p[u], ss);
+          const float r = rsqrtf(group_sum(sum4(ss), w.lanes) / a.D + a.eps);
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) p[u] = times(scaled(p[u], r), weight[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          if (!there[k] || !at[u].on) continue;
+          if (at[u].turned) p[u] = rotate(p[u], turn[u]);
+          F4 x, y;
+          as_quads<kInter>(p[u], x, y);
+          Raw oa = Four<T>::put(x), ob = Four<T>::put(y);
+          if (!kNorm && !at[u].turned) oa = ra[k][u], ob = rb[k][u];  // a copy
+          *reinterpret_cast<Raw*>(to_head + at[u].a) = oa;
+          *reinterpret_cast<Raw*>(to_head + at[u].b) = ob;
+        }
+      }
+    }
+  }
+}
+
+// ---- gradients ------------------------------------------------------------------------------
+// Warps walk the items with a stride and keep the weight gradients of their lanes' channels;
+// a block adds its groups and warps in a fixed order and writes one row for q and one for k.
+template <typename T, bool kInter, int kUnits>
+__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
+  __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
+  __shared__ __align__(16) float sums[kWarps][2][256];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int group = lane / w.lanes, groups = 32 / w.lanes, within = lane & (w.lanes - 1);
+  const float inv_d = 1.f / a.D;
+  Unit at[kUnits];
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) at[u] = unit<kInter>(a, u * w.lanes + within);
+  Pairs dw[2][kUnits];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) dw[i][u] = Pairs{all4(0.f), all4(0.f)};
+  const int steps = w.q_steps + w.k_steps;
+  for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < w.items; item += (int64_t)gridDim.x * kWarps) {
+    const int64_t row = w.parts == 1 ? item : item / w.parts;
+    const int part = (int)(item - row * w.parts);
+    __syncwarp();  // the angles of the item before have been read
+    angles(a, row, cs[warp]);
     __syncwarp();
-    float ss = 0.f, dot = 0.f;
-    for (int c = lane; c < a.D; c += 32) {
-      const float xv = ld(in + c);
-      ss = fmaf(xv, xv, ss);
-      dot = fmaf(xv, dy[w][c] * t.weight[c], dot);
+    Turn turn[kUnits];
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u)
+      if (at[u].turned) turn[u] = turn_of(cs[warp] + 4 * (u * w.lanes + within));
+    const int first = (int)((int64_t)steps * part / w.parts), last = (int)((int64_t)steps * (part + 1) / w.parts);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const HeadRows& t = which ? a.k : a.q;
+      const int from = which ? max(first - w.q_steps, 0) : first, to = which ? last - w.q_steps : min(last, w.q_steps);
+      if (from >= to) continue;
+      const T* in = static_cast<const T*>(t.in) + row * t.stride;
+      const T* grad = static_cast<const T*>(t.grad) + row * t.grad_stride;
+      T* out = static_cast<T*>(t.out) + row * t.out_stride;
+      Pairs weight[kUnits];
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u)
+        if (at[u].on) weight[u] = as_pairs<kInter>(load4(t.weight + at[u].a), load4(t.weight + at[u].b));
+#pragma unroll 2
+      for (int step = from; step < to; ++step) {
+        const int head = step * groups + group;
+        const bool there = head < t.H;
+        Pairs x[kUnits], g[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          x[u] = g[u] = Pairs{all4(0.f), all4(0.f)};
+          if (there && at[u].on) {
+            x[u] = as_pairs<kInter>(load4(in + head * a.D + at[u].a), load4(in + head * a.D + at[u].b));
+            g[u] = as_pairs<kInter>(load4(grad + head * a.D + at[u].a), load4(grad + head * a.D + at[u].b));
+          }
+        }
+        F4 ss = all4(0.f), dot = all4(0.f);
+        Pairs wg[kUnits];
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          if (at[u].turned) g[u] = rotate_back(g[u], turn[u]);
+          wg[u] = at[u].on ? times(g[u], weight[u]) : g[u];
+          ss = dot4(x[u], x[u], ss);
+          dot = dot4(x[u], wg[u], dot);
+        }
+        const float r = rsqrtf(group_sum(sum4(ss), w.lanes) * inv_d + a.eps);
+        const float m = group_sum(sum4(dot), w.lanes) * r * inv_d;
+#pragma unroll
+        for (int u = 0; u < kUnits; ++u) {
+          if (!there || !at[u].on) continue;
+          const Pairs n = scaled(x[u], r);
+          dw[which][u] = Pairs{fma4(g[u].x, n.x, dw[which][u].x), fma4(g[u].y, n.y, dw[which][u].y)};
+          Pairs d{fma4(n.x, all4(-m), wg[u].x), fma4(n.y, all4(-m), wg[u].y)};
+          d = scaled(d, r);
+          F4 p, q;
+          as_quads<kInter>(d, p, q);
+          store4(out + head * a.D + at[u].a, p);
+          store4(out + head * a.D + at[u].b, q);
+        }
+      }
     }
-    const float r = rsqrtf(warp_sum(ss) / a.D + a.eps);
-    const float m = warp_sum(dot) * r / a.D;
-    for (int c = lane; c < a.D; c += 32) {
-      const float n = ld(in + c) * r;
-      dw[w][which][c] = fmaf(dy[w][c], n, dw[w][which][c]);
-      st(out + c, r * (dy[w][c] * t.weight[c] - n * m));
+  }
+  // Groups of a warp (the same channels in lanes w.lanes apart), then warps.
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+#pragma unroll
+    for (int u = 0; u < kUnits; ++u) {
+      F4 p, q;
+      as_quads<kInter>(dw[which][u], p, q);
+      float v[8] = {p.a.x, p.a.y, p.b.x, p.b.y, q.a.x, q.a.y, q.b.x, q.b.y};
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        for (int o = w.lanes; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+      if (group == 0 && at[u].on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sums[warp][which][at[u].a + i] = v[i];
+          sums[warp][which][at[u].b + i] = v[4 + i];
+        }
+      }
     }
-    __syncwarp();
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * a.D; c += 256) {
-    const int which = c / a.D, ch = c - which * a.D;
+  for (int c = threadIdx.x; c < 2 * a.D; c += kThreads) {
+    const int which = c >= a.D, ch = c - which * a.D;
     float s = 0.f;
-    for (int i = 0; i < 8; ++i) s += dw[i][which][ch];
-    part[((int64_t)which * gridDim.x + blockIdx.x) * a.D + ch] = s;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) s += sums[i][which][ch];
+    part_sums[((int64_t)which * gridDim.x + blockIdx.x) * a.D + ch] = s;
   }
 }
 
-__global__ void qk_weight_grad_k(QkRopeArgs a, const float* part, int blocks) {
-  const int which = blockIdx.x;
-  float* dw = which ? a.k.dweight : a.q.dweight;
-  for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
-    float s = 0.f;
-    for (int b = 0; b < blocks; ++b) s += part[((int64_t)which * blocks + b) * a.D + c];
-    dw[c] = s;
-  }
+// The blocks' rows: 32 lanes of rows by 8 channels a block, then a tree over the lanes.
+__global__ void __launch_bounds__(256) qk_weight_grad_k(QkRopeArgs a, const float* part, int blocks) {
+  const int which = blockIdx.y, ch = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const float* p = part + (int64_t)which * blocks * a.D + ch;
+  float s = 0.f;
+  for (int b = lane; b < blocks; b += 32) s += p[(int64_t)b * a.D];
+  s = group_sum(s, 32);
+  if (lane == 0) (which ? a.k.dweight : a.q.dweight)[ch] = s;
+}
+
+// ---- launch -----------------------------------------------------------------------------------
+
+int units_of(const QkRopeArgs& a) {  // units a lane takes: 1 or 3
+  const int n = a.D / 8;
+  int p = 1;
+  while (p < n) p *= 2;
+  return p >= 4 && n <= p / 4 * 3 ? 3 : 1;
+}
+Split split(const QkRopeArgs& a, int units, int64_t warps) {
+  const int n = a.D / 8;
+  Split w;
+  w.lanes = 1;
+  while (w.lanes * units < n) w.lanes *= 2;
+  const int groups = 32 / w.lanes;
+  w.q_steps = (a.q.H + groups - 1) / groups;
+  w.k_steps = (a.k.H + groups - 1) / groups;
+  // Tokens are shared between warps until `warps` of them have work.
+  w.parts = (int)std::max<int64_t>(1, std::min<int64_t>(w.q_steps + w.k_steps, warps / a.rows));
+  w.items = a.rows * w.parts;
+  return w;
+}
+
+template <typename T, bool kNorm, bool kInter, int kUnits>
+cudaError_t forward(const QkRopeArgs& a, cudaStream_t s) {
+  constexpr int kHeads = kUnits == 1 ? 4 : 2;
+  const Split w = split(a, kUnits, 148 * 16);
+  qk_rope_k<T, kNorm, kInter, kUnits, kHeads><<<(unsigned)((w.items + kWarps - 1) / kWarps), kThreads, 0, s>>>(a, w);
+  return cudaGetLastError();
+}
+template <typename T, bool kNorm>
+cudaError_t forward_by(const QkRopeArgs& a, cudaStream_t s) {
+  if (units_of(a) == 1) return a.interleaved ? forward<T, kNorm, true, 1>(a, s) : forward<T, kNorm, false, 1>(a, s);
+  return a.interleaved ? forward<T, kNorm, true, 3>(a, s) : forward<T, kNorm, false, 3>(a, s);
+}
+
+constexpr int kBwdBlocks = 148 * 6;
+int bwd_blocks(const Split& w) { return (int)std::min<int64_t>(kBwdBlocks, (w.items + kWarps - 1) / kWarps); }
+
+template <typename T, bool kInter, int kUnits>
+cudaError_t backward(const QkRopeArgs& a, float* part, cudaStream_t s) {
+  const Split w = split(a, kUnits, 148 * 16);
+  const int blocks = bwd_blocks(w);
+  qk_norm_rope_bwd_k<T, kInter, kUnits><<<blocks, kThreads, 0, s>>>(a, w, part);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  qk_weight_grad_k<<<dim3(a.D / 8, a.k.H ? 2 : 1), 256, 0, s>>>(a, part, blocks);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t backward_by(const QkRopeArgs& a, float* part, cudaStream_t s) {
+  if (units_of(a) == 1) return a.interleaved ? backward<T, true, 1>(a, part, s) : backward<T, false, 1>(a, part, s);
+  return a.interleaved ? backward<T, true, 3>(a, part, s) : backward<T, false, 3>(a, part, s);
 }
 
 }  // namespace
 
 cudaError_t qk_rope_launch(const QkRopeArgs& a, cudaStream_t s) {
-  const int64_t items = a.rows * (a.q.H + a.k.H);
-  const unsigned grid = (unsigned)((items + 3) / 4);
-  if (a.bf16)
-    qk_rope_k<__nv_bfloat16><<<grid, 128, 0, s>>>(a);
-  else
-    qk_rope_k<float><<<grid, 128, 0, s>>>(a);
-  return cudaGetLastError();
+  if (a.q.weight) return a.bf16 ? forward_by<__nv_bfloat16, true>(a, s) : forward_by<float, true>(a, s);
+  return a.bf16 ? forward_by<__nv_bfloat16, false>(a, s) : forward_by<float, false>(a, s);
 }
 
-size_t qk_norm_rope_bwd_workspace_bytes(const QkRopeArgs& a) { return (size_t)kBwdBlocks * 2 * a.D * sizeof(float); }
+size_t qk_norm_rope_bwd_workspace_bytes(const QkRopeArgs& a) {
+  return (size_t)bwd_blocks(split(a, units_of(a), 148 * 16)) * 2 * a.D * sizeof(float);
+}
 
 cudaError_t qk_norm_rope_bwd_launch(const QkRopeArgs& a, void* workspace, cudaStream_t s) {
   float* part = static_cast<float*>(workspace);
-  if (a.bf16)
-    qk_norm_rope_bwd_k<__nv_bfloat16><<<kBwdBlocks, 256, 0, s>>>(a, part);
-  else
-    qk_norm_rope_bwd_k<float><<<kBwdBlocks, 256, 0, s>>>(a, part);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  qk_weight_grad_k<<<a.k.H ? 2 : 1, 256, 0, s>>>(a, part, kBwdBlocks);
-  return cudaGetLastError();
+  return a.bf16 ? backward_by<__nv_bfloat16>(a, part, s) : backward_by<float>(a, part, s);
 }
 
 }  // namespace dig

@@ -283,107 +283,135 @@ def dwconv3x3(x, w, out=None, stream=None):
 # ---- gated linear recurrence (vector state) -----------------------------------------
 
 
-def _row_stride(t: torch.Tensor, name: str, lead: int) -> int:
-    """Elements between token rows of t, whose first `lead` dimensions are tokens (batches
-    behind one another without a gap) and whose other dimensions are dense."""
-    inner = 1
-    for d in range(t.dim() - 1, lead - 1, -1):
-        if t.shape[d] != 1 and t.stride(d) != inner:
-            raise ValueError(f"{name}: the channels of a token must be contiguous")
-        inner *= t.shape[d]
-    step, tokens = None, 1
-    for d in range(lead - 1, -1, -1):
-        if t.shape[d] != 1:
-            if step is None:
-                step = t.stride(d)
-            elif t.stride(d) != step * tokens:
-                raise ValueError(f"{name}: its tokens must be equally spaced in memory")
-        tokens *= t.shape[d]
-    return inner if step is None else step
+# A call of a small shape is bound by the host, so the checks below read each property of a
+# tensor once and leave the wording of a refusal to _refuse.
+_Tensor = torch.Tensor
 
 
-def _on(t, name: str, dtype: torch.dtype, dev: torch.device):
+def _refuse(t, name: str, dtype: torch.dtype, dev: torch.device, contiguous: bool = True):
+    """Raises what is wrong with t; ValueError about its layout if nothing else is."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != dev or dev.type != "cuda":
         raise ValueError(f"{name} must be on {dev if dev.type == 'cuda' else 'a CUDA device'} (got {t.device})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    raise ValueError(f"{name} must be contiguous" if contiguous else f"{name}: unsupported layout")
+
+
+def _on(t, name: str, dtype: torch.dtype, dev: torch.device, index: int):
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index >= 0):
+        _refuse(t, name, dtype, dev, False)
+
+
+def _dense(t, name: str, dtype: torch.dtype, dev: torch.device, index: int, shape):
+    """Checks a dense tensor of a given shape."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index >= 0 and t.is_contiguous()):
+        _refuse(t, name, dtype, dev)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+
+
+def _row_stride(t: torch.Tensor, name: str, lead: int, inner: int) -> int:
+    """Elements between token rows of t, whose first `lead` dimensions are tokens (batches
+    behind one another without a gap) and whose other dimensions are dense, `inner` elements."""
+    if t.is_contiguous():
+        return inner
+    shape, stride = t.shape, t.stride()
+    dense = 1
+    for d in range(len(shape) - 1, lead - 1, -1):
+        if shape[d] != 1 and stride[d] != dense:
+            raise ValueError(f"{name}: the channels of a token must be contiguous")
+        dense *= shape[d]
+    step, tokens = None, 1
+    for d in range(lead - 1, -1, -1):
+        if shape[d] != 1:
+            if step is None:
+                step = stride[d]
+            elif stride[d] != step * tokens:
+                raise ValueError(f"{name}: its tokens must be equally spaced in memory")
+        tokens *= shape[d]
+    return inner if step is None else step
 
 
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _call(fn: str, dev: torch.device, stream, *args):
-    if dev.index == torch.cuda.current_device():
-        rc = getattr(_lib, fn)(*args, _stream_handle(dev, stream))
+# The current device and its current stream without the Stream object that
+# torch.cuda.current_stream builds (a microsecond a call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(fn, dev: torch.device, index: int, stream, *args):
+    """fn(*args, stream) with `dev` current; an error status raises."""
+    if index == _current_device():
+        rc = fn(*args, _raw_stream(index) if stream is None else _stream_handle(dev, stream))
     else:
         with torch.cuda.device(dev):
-            rc = getattr(_lib, fn)(*args, _stream_handle(dev, stream))
-    _check(fn, rc)
-
-
-def _like(t, name: str, shape, dtype: torch.dtype, dev: torch.device):
-    """A dense output: the caller's `t`, or a new tensor."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, dtype, dev)
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
-    return t
-
-
-def _optional(t, name: str, shape, dev: torch.device):
-    """An optional dense fp32 input."""
-    if t is not None:
-        _need(t, name, torch.float32, dev)
-        if tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
+            rc = fn(*args, _stream_handle(dev, stream))
+    if rc != 0:
+        raise GlaError(fn.__name__, rc)
 
 
 def _gated(x, gate, gate_norm, dims: int):
-    """Checks x and gate; (dtype code, gate_norm for the C call, their row strides)."""
-    if not isinstance(x, torch.Tensor):
+    """Checks x and gate; (device, its index, shape, dtype code, gate_norm for the C call, row strides)."""
+    if not isinstance(x, _Tensor):
         raise TypeError("x must be a torch.Tensor")
+    dtype, dev, index, shape = x.dtype, x.device, x.get_device(), x.shape
     dt = _grid_dtype(x)
-    _on(x, "x", x.dtype, x.device)
-    if gate_norm is not None and not (0.0 < gate_norm < math.inf):
-        raise ValueError("gate_norm must be positive and finite (None: gate holds log_alpha)")
-    _on(gate, "gate", torch.float32 if gate_norm is None else x.dtype, x.device)
-    if x.dim() != dims or gate.shape != x.shape:
+    if index < 0:
+        _refuse(x, "x", dtype, dev)
+    if gate_norm is None:
+        norm, gtype = 0.0, torch.float32
+    else:
+        norm, gtype = float(gate_norm), dtype
+        if not 0.0 < norm < math.inf:
+            raise ValueError("gate_norm must be positive and finite (None: gate holds log_alpha)")
+    _on(gate, "gate", gtype, dev, index)
+    if len(shape) != dims or gate.shape != shape:
         raise ValueError(f"expected x and gate of the same {dims}-dimensional shape")
-    if max(x.shape) >= 1 << 31:
+    if max(shape) >= 1 << 31:
         raise ValueError("x: a dimension of 2^31 or more")
-    return dt, 0.0 if gate_norm is None else float(gate_norm), _row_stride(x, "x", dims - 1), _row_stride(gate, "gate", dims - 1)
+    C = shape[-1]
+    return dev, index, shape, dt, norm, _row_stride(x, "x", dims - 1, C), _row_stride(gate, "gate", dims - 1, C)
 
 
-def _glr_where(x, where):
-    """(leading C arguments, sequences, packed?) of a grid (Hgrid, Wgrid) or of cu_seqlens."""
-    if len(where) == 2:
-        B, T, C = x.shape
-        Hgrid, Wgrid = where
-        if T != Hgrid * Wgrid:
-            raise ValueError(f"T={T} does not match the grid {Hgrid}x{Wgrid}")
-        return (B, Hgrid, Wgrid, C), B
-    cu, = where
-    _need(cu, "cu_seqlens", torch.int32, x.device)
-    if cu.dim() != 1 or cu.numel() < 2:
+def _grid_sizes(shape, Hgrid, Wgrid):
+    if shape[1] != Hgrid * Wgrid:
+        raise ValueError(f"T={shape[1]} does not match the grid {Hgrid}x{Wgrid}")
+    return (shape[0], Hgrid, Wgrid, shape[2]), shape[0]
+
+
+def _packed_sizes(shape, cu, dev, index):
+    n = cu.numel() - 1 if isinstance(cu, _Tensor) else 0
+    _dense(cu, "cu_seqlens", torch.int32, dev, index, (n + 1,))
+    if n < 1:
         raise ValueError("cu_seqlens must be [sequences + 1]")
-    return (x.shape[0], cu.numel() - 1, x.shape[1]), cu.numel() - 1
+    return (shape[0], n, shape[1]), n
 
 
 def _glr_fwd(fn, x, gate, where, direction, gate_norm, complement, h0, out, h_last, stream):
     packed = len(where) == 1
-    dt, norm, xs, gs = _gated(x, gate, gate_norm, 2 if packed else 3)
-    sizes, n = _glr_where(x, where)
-    dev, C = x.device, x.shape[-1]
-    _optional(h0, "h0", (n, C), dev)
-    fill = (int(out is None),) if packed else ()
-    out = _like(out, "out", x.shape, x.dtype, dev)
-    h_last = _like(h_last, "h_last", (n, C), torch.float32, dev)
-    _call(fn, dev, stream, x.data_ptr(), gate.data_ptr(), *map(_ptr, where[:packed]), _ptr(h0), *sizes, xs, gs,
-          int(direction), norm, int(bool(complement)), dt, *fill, out.data_ptr(), h_last.data_ptr())
+    dev, index, shape, dt, norm, xs, gs = _gated(x, gate, gate_norm, 2 if packed else 3)
+    sizes, n = _packed_sizes(shape, where[0], dev, index) if packed else _grid_sizes(shape, *where)
+    states = (n, shape[-1])
+    if h0 is not None:
+        _dense(h0, "h0", torch.float32, dev, index, states)
+    fill = out is None
+    if fill:
+        out = x.new_empty(shape)
+    else:
+        _dense(out, "out", x.dtype, dev, index, shape)
+    if h_last is None:
+        h_last = torch.empty(states, dtype=torch.float32, device=dev)
+    else:
+        _dense(h_last, "h_last", torch.float32, dev, index, states)
+    _call(fn, dev, index, stream, x.data_ptr(), gate.data_ptr(), *((where[0].data_ptr(),) if packed else ()), _ptr(h0),
+          *sizes, xs, gs, int(direction), norm, int(bool(complement)), dt, *((int(fill),) if packed else ()),
+          out.data_ptr(), h_last.data_ptr())
     return out, h_last
 
 
@@ -394,7 +422,7 @@ def glr_fwd(x, gate, Hgrid: int, Wgrid: int, direction: int, gate_norm: float | 
     gate [B,T,C]: log_alpha in fp32 (gate_norm None), or logits of x's type with log_alpha =
     logsigmoid(gate) / gate_norm.  complement: s = 1 - alpha instead of 1.  h0 [B,C] fp32.
     Returns (out [B,T,C], h_last [B,C] fp32); h_last may be given as h0 to carry a state in place."""
-    return _glr_fwd("glr_fwd", x, gate, (Hgrid, Wgrid), direction, gate_norm, complement, h0, out, h_last, stream)
+    return _glr_fwd(_lib.glr_fwd, x, gate, (Hgrid, Wgrid), direction, gate_norm, complement, h0, out, h_last, stream)
 
 
 def glr_fwd_packed(x, gate, cu_seqlens, direction: int = 0, gate_norm: float | None = None, complement: bool = False,
@@ -402,29 +430,39 @@ def glr_fwd_packed(x, gate, cu_seqlens, direction: int = 0, gate_norm: float | N
     """glr_fwd over packed sequences: x, gate [rows,C], cu_seqlens int32 [n+1] on the device,
     direction 0 or 1, h0 and h_last [n,C].  Rows of no sequence: left as they were in a given
     `out`, zero in a new one."""
-    return _glr_fwd("glr_fwd_packed", x, gate, (cu_seqlens,), direction, gate_norm, complement, h0, out, h_last, stream)
+    return _glr_fwd(_lib.glr_fwd_packed, x, gate, (cu_seqlens,), direction, gate_norm, complement, h0, out, h_last, stream)
 
 
 def _glr_bwd(fn, x, gate, h, dout, where, direction, gate_norm, complement, h0, dh_last, outs, stream):
     packed = len(where) == 1
-    dt, norm, xs, gs = _gated(x, gate, gate_norm, 2 if packed else 3)
-    sizes, n = _glr_where(x, where)
-    dev, C = x.device, x.shape[-1]
-    for t, name in ((h, "h"), (dout, "dout")):
-        _need(t, name, x.dtype, dev)
-        if t.shape != x.shape:
-            raise ValueError(f"{name} must have x's shape")
-    _optional(h0, "h0", (n, C), dev)
-    _optional(dh_last, "dh_last", (n, C), dev)
-    if packed and (outs[0] is None) != (outs[1] is None):
+    dev, index, shape, dt, norm, xs, gs = _gated(x, gate, gate_norm, 2 if packed else 3)
+    sizes, n = _packed_sizes(shape, where[0], dev, index) if packed else _grid_sizes(shape, *where)
+    states = (n, shape[-1])
+    _dense(h, "h", x.dtype, dev, index, shape)
+    _dense(dout, "dout", x.dtype, dev, index, shape)
+    if h0 is not None:
+        _dense(h0, "h0", torch.float32, dev, index, states)
+    if dh_last is not None:
+        _dense(dh_last, "dh_last", torch.float32, dev, index, states)
+    dx, dgate, dh0 = outs
+    if packed and (dx is None) != (dgate is None):
         raise ValueError("give both dx and dgate, or neither")
-    fill = (int(outs[0] is None),) if packed else ()
-    dx = _like(outs[0], "dx", x.shape, x.dtype, dev)
-    dgate = _like(outs[1], "dgate", x.shape, gate.dtype, dev)
-    dh0 = _like(outs[2], "dh0", (n, C), torch.float32, dev)
-    _call(fn, dev, stream, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dout.data_ptr(), *map(_ptr, where[:packed]),
-          _ptr(h0), _ptr(dh_last), *sizes, xs, gs, int(direction), norm, int(bool(complement)), dt, *fill,
-          dx.data_ptr(), dgate.data_ptr(), dh0.data_ptr())
+    fill = dx is None
+    if fill:
+        dx = x.new_empty(shape)
+    else:
+        _dense(dx, "dx", x.dtype, dev, index, shape)
+    if dgate is None:
+        dgate = gate.new_empty(shape)
+    else:
+        _dense(dgate, "dgate", gate.dtype, dev, index, shape)
+    if dh0 is None:
+        dh0 = torch.empty(states, dtype=torch.float32, device=dev)
+    else:
+        _dense(dh0, "dh0", torch.float32, dev, index, states)
+    _call(fn, dev, index, stream, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dout.data_ptr(),
+          *((where[0].data_ptr(),) if packed else ()), _ptr(h0), _ptr(dh_last), *sizes, xs, gs, int(direction), norm,
+          int(bool(complement)), dt, *((int(fill),) if packed else ()), dx.data_ptr(), dgate.data_ptr(), dh0.data_ptr())
     return dx, dgate, dh0
 
 
@@ -433,7 +471,7 @@ def glr_bwd(x, gate, h, dout, Hgrid: int, Wgrid: int, direction: int, gate_norm:
     """The gradients of sum(dout * out) + sum(dh_last * h_last) for (out, h_last) = glr_fwd(x, gate,
     ...), with h = that out (see include/dig_gla.h, glr_bwd).  Returns (dx of x's type, dgate of
     gate's type, dh0 fp32 [B,C])."""
-    return _glr_bwd("glr_bwd", x, gate, h, dout, (Hgrid, Wgrid), direction, gate_norm, complement, h0, dh_last,
+    return _glr_bwd(_lib.glr_bwd, x, gate, h, dout, (Hgrid, Wgrid), direction, gate_norm, complement, h0, dh_last,
                     (dx, dgate, dh0), stream)
 
 
@@ -441,7 +479,7 @@ def glr_bwd_packed(x, gate, h, dout, cu_seqlens, direction: int = 0, gate_norm: 
                    complement: bool = False, h0=None, dh_last=None, dx=None, dgate=None, dh0=None, stream=None):
     """glr_bwd over packed sequences.  Rows of no sequence: left as they were in given dx and
     dgate, zero in new ones."""
-    return _glr_bwd("glr_bwd_packed", x, gate, h, dout, (cu_seqlens,), direction, gate_norm, complement, h0, dh_last,
+    return _glr_bwd(_lib.glr_bwd_packed, x, gate, h, dout, (cu_seqlens,), direction, gate_norm, complement, h0, dh_last,
                     (dx, dgate, dh0), stream)
 
 
@@ -451,21 +489,24 @@ def glr_step(x, gate, state, slots=None, gate_norm: float | None = None, complem
     state [nslots,C] fp32; slots int32 [N] (None: row i uses state i; negative: a padded row).
     Updates `state` in place, or writes the new states to `state_out`.  Returns (out [N,C], the
     updated pool); padded rows are left as they were in a given `out`, zero in a new one."""
-    dt, norm, xs, gs = _gated(x, gate, gate_norm, 2)
-    dev = x.device
-    N, C = x.shape
-    _need(state, "state", torch.float32, dev)
-    if state.dim() != 2 or state.shape[1] != C:
-        raise ValueError("state must be [nslots, C]")
+    dev, index, shape, dt, norm, xs, gs = _gated(x, gate, gate_norm, 2)
+    N, C = shape
+    nslots = state.shape[0] if isinstance(state, _Tensor) and state.dim() else 0
+    pool = (nslots, C)
+    _dense(state, "state", torch.float32, dev, index, pool)
     if slots is not None:
-        _need(slots, "slots", torch.int32, dev)
-        if tuple(slots.shape) != (N,):
-            raise ValueError("slots must be [N]")
-    fill = int(out is None)
-    out = _like(out, "out", (N, C), x.dtype, dev)
-    state_out = state if state_out is None else _like(state_out, "state_out", state.shape, torch.float32, dev)
-    _call("glr_step", dev, stream, x.data_ptr(), gate.data_ptr(), state.data_ptr(), _ptr(slots), N, state.shape[0], C,
-          xs, gs, norm, int(bool(complement)), dt, fill, state_out.data_ptr(), out.data_ptr())
+        _dense(slots, "slots", torch.int32, dev, index, (N,))
+    fill = out is None
+    if fill:
+        out = x.new_empty(shape)
+    else:
+        _dense(out, "out", x.dtype, dev, index, shape)
+    if state_out is None:
+        state_out = state
+    else:
+        _dense(state_out, "state_out", torch.float32, dev, index, pool)
+    _call(_lib.glr_step, dev, index, stream, x.data_ptr(), gate.data_ptr(), state.data_ptr(), _ptr(slots), N, nslots, C,
+          xs, gs, norm, int(bool(complement)), dt, int(fill), state_out.data_ptr(), out.data_ptr())
     return out, state_out
 
 
@@ -515,62 +556,68 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     return inv.to(torch.float32).to(device or "cpu"), scale
 
 
-def _heads(t, name: str, like):
-    """Checks a tensor of heads [..., H, D]; its row stride."""
-    _on(t, name, like.dtype, like.device)
-    if t.dim() != like.dim() or t.dim() not in (3, 4) or t.shape[:-2] != like.shape[:-2] or t.shape[-1] != like.shape[-1]:
+def _heads(t, name: str, dtype, dev, index: int, lead, D: int):
+    """Checks a tensor of heads [*lead, H, D]; (H, its row stride)."""
+    _on(t, name, dtype, dev, index)
+    shape = t.shape
+    if len(shape) != len(lead) + 2 or shape[-1] != D or shape[:-2] != lead:
         raise ValueError(f"{name}: expected [rows,H,D] or [B,T,H,D] with the rows and D of the queries")
-    return _row_stride(t, name, t.dim() - 2)
+    return shape[-2], _row_stride(t, name, len(lead), shape[-2] * D)
 
 
-def _head_out(t, name: str, like):
+def _head_out(t, name: str, like, dtype, dev, index: int, lead, H: int, D: int):
     """A caller's output of `like`'s shape, or a new dense one; with its row stride."""
     if t is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device), like.shape[-1] * like.shape[-2]
-    s = _heads(t, name, like)
-    if t.shape != like.shape:
+        return like.new_empty(like.shape), H * D
+    h, stride = _heads(t, name, dtype, dev, index, lead, D)
+    if h != H:
         raise ValueError(f"{name} must be {list(like.shape)} (got {list(t.shape)})")
-    return t, s
+    return t, stride
 
 
-def _angles(q, positions, inv_freq):
-    """C arguments of the positions and the table, and rows, D, rot."""
-    if not isinstance(q, torch.Tensor):
+def _queries(q):
+    """(device, its index, dtype, dtype code, leading dimensions, rows, D) of the queries."""
+    if not isinstance(q, _Tensor):
         raise TypeError("q must be a torch.Tensor")
-    _grid_dtype(q)
-    if q.dim() not in (3, 4):
+    dt, shape, dev, index = _grid_dtype(q), q.shape, q.device, q.get_device()
+    if len(shape) not in (3, 4):
         raise ValueError("q: expected [rows,H,D] or [B,T,H,D]")
-    rows = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    if index < 0:
+        _refuse(q, "q", q.dtype, dev)
+    lead = shape[:-2]
+    return dev, index, q.dtype, dt, lead, lead.numel(), shape[-1]
+
+
+def _angle_args(positions, inv_freq, dev, index, lead, rows):
+    """C arguments of the positions and the table, and rot."""
+    at, wide = None, 0
     if positions is not None:
-        if not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64):
+        if not isinstance(positions, _Tensor) or positions.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be an int32 or int64 tensor")
-        _need(positions, "positions", positions.dtype, q.device)
-        if positions.shape != q.shape[:-2]:
-            raise ValueError("positions must be one for each row of q")
-    rot = 0
+        wide = int(positions.dtype is torch.int64)
+        _dense(positions, "positions", positions.dtype, dev, index, lead)
+        at = positions.data_ptr()
+    rot, table = 0, None
     if inv_freq is not None:
-        _need(inv_freq, "inv_freq", torch.float32, q.device)
-        if inv_freq.dim() != 1:
-            raise ValueError("inv_freq must be [rot/2]")
-        rot = 2 * inv_freq.numel()
-    period = q.shape[-3]
-    return (_ptr(positions), int(positions is not None and positions.dtype == torch.int64), period, _ptr(inv_freq),
-            rows), rot
+        rot = 2 * inv_freq.numel() if isinstance(inv_freq, _Tensor) else 0
+        _dense(inv_freq, "inv_freq", torch.float32, dev, index, (rot // 2,))
+        table = inv_freq.data_ptr()
+    return (at, wide, lead[-1], table, rows), rot
 
 
 def _rope_call(fn, q, k, weights, positions, inv_freq, middle, q_out, k_out, stream):
-    lead, rot = _angles(q, positions, inv_freq)
-    H, D = q.shape[-2:]
-    qs = _heads(q, "q", q)
-    q_out, qos = _head_out(q_out, "q_out", q)
-    ks, Hk, kos = H * D, 0, H * D
+    dev, index, dtype, dt, lead, rows, D = _queries(q)
+    angles, rot = _angle_args(positions, inv_freq, dev, index, lead, rows)
+    w = _weights(k, *weights, dev, index, D) if weights else ()
+    H, qs = _heads(q, "q", dtype, dev, index, lead, D)
+    q_out, qos = _head_out(q_out, "q_out", q, dtype, dev, index, lead, H, D)
+    Hk, ks, kos = 0, D, D
     if k is not None:
-        ks = _heads(k, "k", q)
-        Hk = k.shape[-2]
-        k_out, kos = _head_out(k_out, "k_out", k)
+        Hk, ks = _heads(k, "k", dtype, dev, index, lead, D)
+        k_out, kos = _head_out(k_out, "k_out", k, dtype, dev, index, lead, Hk, D)
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call(fn, q.device, stream, q.data_ptr(), _ptr(k), *weights, *lead, H, Hk, D, rot, qs, ks, *middle, _grid_dtype(q),
+    _call(fn, dev, index, stream, q.data_ptr(), _ptr(k), *w, *angles, H, Hk, D, rot, qs, ks, *middle, dt,
           q_out.data_ptr(), qos, _ptr(k_out), kos)
     return q_out, k_out
 
@@ -582,20 +629,18 @@ def rope(q, k, positions, inv_freq, interleaved: bool = False, scale: float = 1.
     projection; positions int32/int64, one a row (None: 0..T-1 in every batch); inv_freq
     fp32 [rot/2] (rope_frequencies).  inverse: turns back, the gradient.  q_out, k_out may be q
     and k.  Returns (q_out, k_out)."""
-    return _rope_call("rope", q, k, (), positions, inv_freq, (int(bool(interleaved)), int(bool(inverse)), float(scale)),
+    return _rope_call(_lib.rope, q, k, (), positions, inv_freq, (int(bool(interleaved)), int(bool(inverse)), float(scale)),
                       q_out, k_out, stream)
 
 
-def _weights(q, k, q_weight, k_weight):
-    for w, name, t in ((q_weight, "q_weight", q), (k_weight, "k_weight", k)):
-        if t is None:
-            if w is not None:
-                raise ValueError(f"{name} without its heads")
-            continue
-        _need(w, name, torch.float32, q.device)
-        if w.dim() != 1 or w.shape[0] != q.shape[-1]:
-            raise ValueError(f"{name} must be [D]")
-    return _ptr(q_weight), _ptr(k_weight)
+def _weights(k, q_weight, k_weight, dev, index, D):
+    _dense(q_weight, "q_weight", torch.float32, dev, index, (D,))
+    if k is not None:
+        _dense(k_weight, "k_weight", torch.float32, dev, index, (D,))
+        return q_weight.data_ptr(), k_weight.data_ptr()
+    if k_weight is not None:
+        raise ValueError("k_weight without its heads")
+    return q_weight.data_ptr(), None
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-6, interleaved: bool = False,
@@ -603,9 +648,7 @@ def qk_norm_rope(q, k, q_weight, k_weight, positions, inv_freq, eps: float = 1e-
     """RMS norm of every query and key head, then rope, in one pass (see include/dig_gla.h,
     qk_norm_rope).  q_weight, k_weight fp32 [D]; inv_freq None: the norm alone.  The rest as rope.
     Returns (q_out, k_out)."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q must be a torch.Tensor")
-    return _rope_call("qk_norm_rope", q, k, _weights(q, k, q_weight, k_weight), positions, inv_freq,
+    return _rope_call(_lib.qk_norm_rope, q, k, (q_weight, k_weight), positions, inv_freq,
                       (int(bool(interleaved)), float(eps), float(scale)), q_out, k_out, stream)
 
 
@@ -614,26 +657,28 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_fr
     """The gradients of qk_norm_rope (see include/dig_gla.h, qk_norm_rope_bwd) from its inputs and
     those of its outputs.  dq and dk may be dq_out and dk_out.  Returns (dq, dk, dq_weight fp32,
     dk_weight fp32)."""
-    lead, rot = _angles(q, positions, inv_freq)
-    w = _weights(q, k, q_weight, k_weight)
-    H, D = q.shape[-2:]
-    qs, dqs = _heads(q, "q", q), _heads(dq_out, "dq_out", q)
-    if dq_out.shape != q.shape:
+    dev, index, dtype, dt, lead, rows, D = _queries(q)
+    angles, rot = _angle_args(positions, inv_freq, dev, index, lead, rows)
+    w = _weights(k, q_weight, k_weight, dev, index, D)
+    H, qs = _heads(q, "q", dtype, dev, index, lead, D)
+    h, dqs = _heads(dq_out, "dq_out", dtype, dev, index, lead, D)
+    if h != H:
         raise ValueError("dq_out must have q's shape")
-    dq, dqo = _head_out(dq, "dq", q)
-    dwq = torch.empty(D, dtype=torch.float32, device=q.device)
-    Hk, ks, dks, dko, dwk = 0, H * D, H * D, H * D, None
+    dq, dqo = _head_out(dq, "dq", q, dtype, dev, index, lead, H, D)
+    dwq = q_weight.new_empty((D,))
+    Hk, ks, dks, dko, dwk = 0, D, D, D, None
     if k is not None:
-        Hk, ks, dks = k.shape[-2], _heads(k, "k", q), _heads(dk_out, "dk_out", q)
-        if dk_out.shape != k.shape:
+        Hk, ks = _heads(k, "k", dtype, dev, index, lead, D)
+        h, dks = _heads(dk_out, "dk_out", dtype, dev, index, lead, D)
+        if h != Hk:
             raise ValueError("dk_out must have k's shape")
-        dk, dko = _head_out(dk, "dk", k)
-        dwk = torch.empty(D, dtype=torch.float32, device=q.device)
+        dk, dko = _head_out(dk, "dk", k, dtype, dev, index, lead, Hk, D)
+        dwk = q_weight.new_empty((D,))
     elif dk_out is not None or dk is not None:
         raise ValueError("dk_out or dk without k")
-    _call("qk_norm_rope_bwd", q.device, stream, dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), *w, *lead, H, Hk,
-          D, rot, dqs, dks, qs, ks, int(bool(interleaved)), float(eps), float(scale), _grid_dtype(q), dq.data_ptr(), dqo,
-          _ptr(dk), dko, dwq.data_ptr(), _ptr(dwk))
+    _call(_lib.qk_norm_rope_bwd, dev, index, stream, dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), *w, *angles, H,
+          Hk, D, rot, dqs, dks, qs, ks, int(bool(interleaved)), float(eps), float(scale), dt, dq.data_ptr(), dqo, _ptr(dk),
+          dko, dwq.data_ptr(), _ptr(dwk))
     return dq, dk, dwq, dwk
 
 

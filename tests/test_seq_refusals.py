@@ -196,12 +196,12 @@ def test_binding_refuses_cpu_tensors_and_shapes():
 def test_row_stride():
     from gated_linear_attention_chunkwise_b200 import _row_stride
     t = torch.zeros(3, 5, 32)
-    assert _row_stride(t, "t", 2) == 32
-    assert _row_stride(t[..., 8:16], "t", 2) == 32
-    assert _row_stride(t[:1, :, :8], "t", 2) == 32
-    assert _row_stride(t[:, :1, :8], "t", 2) == 160
-    assert _row_stride(t[:1, :1, :8], "t", 2) == 8
-    assert _row_stride(torch.zeros(3, 5, 4, 8)[:, :, 1:3], "t", 2) == 32
+    assert _row_stride(t, "t", 2, 32) == 32
+    assert _row_stride(t[..., 8:16], "t", 2, 8) == 32
+    assert _row_stride(t[:1, :, :8], "t", 2, 8) == 32
+    assert _row_stride(t[:, :1, :8], "t", 2, 8) == 160
+    assert _row_stride(t[:1, :1, :8], "t", 2, 8) == 8
+    assert _row_stride(torch.zeros(3, 5, 4, 8)[:, :, 1:3], "t", 2, 16) == 32
     for bad in (t[:, :4], t[..., ::2], t.transpose(0, 1), t.transpose(1, 2)):
         with pytest.raises(ValueError):
-            _row_stride(bad, "t", 2)
+            _row_stride(bad, "t", 2, bad.shape[2])

@@ -63,7 +63,8 @@ __device__ __forceinline__ Turn turn_of(const float2* cs) {
 
 // ---- units ------------------------------------------------------------------------------
 
-// Where a lane's unit lies in a head: channels a .. a + 3 and b .. b + 3.
+// Where a lane's unit lies in a head: channels a .. a + 3 and b .. b + 3.  A lane behind the
+// last unit reads the last one and keeps nothing (on = false).
 struct Unit {
   int a, b;
   bool on, turned;
@@ -72,6 +73,7 @@ template <bool kInter>
 __device__ __forceinline__ Unit unit(const QkRopeArgs& q, int i) {
   Unit u;
   u.on = i < q.D / 8;
+  i = min(i, q.D / 8 - 1);
   u.turned = i < q.rot / 8;
   const bool halves = !kInter && u.turned;
   u.a = halves ? 4 * i : kInter ? 8 * i : q.rot + 8 * (i - q.rot / 8);
@@ -98,11 +100,13 @@ __device__ __forceinline__ void as_quads(const Pairs& p, F4& a, F4& b) {
     b = p.y;
   }
 }
-__device__ __forceinline__ Pairs rotate(const Pairs& p, const Turn& t) {
-  return Pairs{sub4(mul4(p.x, t.c), mul4(p.y, t.s)), fma4(p.y, t.c, mul4(p.x, t.s))};
-}
-__device__ __forceinline__ Pairs rotate_back(const Pairs& p, const Turn& t) {
-  return Pairs{fma4(p.x, t.c, mul4(p.y, t.s)), sub4(mul4(p.y, t.c), mul4(p.x, t.s))};
+// (x, y) -> (x xc - y ys, y yc + x xs): a turn whose factors may hold weights.
+struct Mix {
+  F4 xc, xs, yc, ys;
+};
+__device__ __forceinline__ F4 minus(F4 v) { return F4{make_float2(-v.a.x, -v.a.y), make_float2(-v.b.x, -v.b.y)}; }
+__device__ __forceinline__ Pairs mix(const Pairs& p, const Mix& t) {
+  return Pairs{fma4(p.y, t.ys, mul4(p.x, t.xc)), fma4(p.x, t.xs, mul4(p.y, t.yc))};
 }
 __device__ __forceinline__ Pairs times(const Pairs& p, const Pairs& q) { return Pairs{mul4(p.x, q.x), mul4(p.y, q.y)}; }
 __device__ __forceinline__ Pairs scaled(const Pairs& p, float f) { return Pairs{mul4(p.x, all4(f)), mul4(p.y, all4(f))}; }
@@ -124,9 +128,18 @@ struct Split {
   int64_t items;   // rows * parts
 };
 
+// The heads of a warp's share of a token: steps [from, to) of q (which = 0) and k (1).
+__device__ __forceinline__ void share(const Split& w, int part, int which, int& from, int& to) {
+  const int steps = w.q_steps + w.k_steps;
+  const int first = w.parts == 1 ? 0 : (int)((int64_t)steps * part / w.parts);
+  const int last = w.parts == 1 ? steps : (int)((int64_t)steps * (part + 1) / w.parts);
+  from = which ? max(first - w.q_steps, 0) : first;
+  to = which ? last - w.q_steps : min(last, w.q_steps);
+}
+
 // ---- forward ------------------------------------------------------------------------------
 template <typename T, bool kNorm, bool kInter, int kUnits, int kHeads>
-__global__ void __launch_bounds__(kThreads) qk_rope_k(QkRopeArgs a, Split w) {
+__global__ void __launch_bounds__(kThreads, kUnits == 1 ? 6 : 4) qk_rope_k(QkRopeArgs a, Split w) {
   using Raw = typename Four<T>::Raw;
   __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -140,67 +153,80 @@ __global__ void __launch_bounds__(kThreads) qk_rope_k(QkRopeArgs a, Split w) {
   for (int u = 0; u < kUnits; ++u) at[u] = unit<kInter>(a, u * w.lanes + within);
   angles(a, row, cs[warp]);
   __syncwarp();
-  Turn turn[kUnits];
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u)
-    if (at[u].turned) turn[u] = turn_of(cs[warp] + 4 * (u * w.lanes + within));
-
-  const int steps = w.q_steps + w.k_steps;
-  const int first = (int)((int64_t)steps * part / w.parts), last = (int)((int64_t)steps * (part + 1) / w.parts);
 #pragma unroll 1
   for (int which = 0; which < 2; ++which) {
     const HeadRows& t = which ? a.k : a.q;
-    const int from = which ? max(first - w.q_steps, 0) : first, to = which ? last - w.q_steps : min(last, w.q_steps);
+    int from, to;
+    share(w, part, which, from, to);
     if (from >= to) continue;
     const T* in = static_cast<const T*>(t.in) + row * t.stride;
     T* out = static_cast<T*>(t.out) + row * t.out_stride;
-    Pairs weight[kUnits];
-    if constexpr (kNorm) {
+    Mix turn[kUnits];  // xc and yc are the weights alone where nothing turns
 #pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-        if (at[u].on) weight[u] = as_pairs<kInter>(load4(t.weight + at[u].a), load4(t.weight + at[u].b));
+    for (int u = 0; u < kUnits; ++u) {
+      if (at[u].turned) {
+        const Turn f = turn_of(cs[warp] + 4 * min(u * w.lanes + within, a.D / 8 - 1));
+        turn[u] = Mix{f.c, f.s, f.c, minus(f.s)};
+      } else {
+        turn[u] = Mix{all4(1.f), all4(0.f), all4(1.f), all4(0.f)};
+      }
+      if constexpr (kNorm) {
+        const Pairs g = as_pairs<kInter>(load4(t.weight + at[u].a), load4(t.weight + at[u].b));
+        turn[u] = Mix{mul4(turn[u].xc, g.x), mul4(turn[u].xs, g.x), mul4(turn[u].yc, g.y), mul4(turn[u].ys, g.y)};
+      }
     }
 #pragma unroll 1
     for (int step = from; step < to; step += kHeads) {
       Raw ra[kHeads][kUnits], rb[kHeads][kUnits];
-      bool there[kHeads];
 #pragma unroll
       for (int k = 0; k < kHeads; ++k) {
-        const int head = (step + k) * groups + group;
-        there[k] = step + k < to && head < t.H;
+        const int head = min((step + k) * groups + group, t.H - 1);
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          ra[k][u] = rb[k][u] = Raw{};
-          if (there[k] && at[u].on) {
-            ra[k][u] = *reinterpret_cast<const Raw*>(in + head * a.D + at[u].a);
-            rb[k][u] = *reinterpret_cast<const Raw*>(in + head * a.D + at[u].b);
+          ra[k][u] = *reinterpret_cast<const Raw*>(in + at[u].a + (int64_t)head * a.D);
+          rb[k][u] = *reinterpret_cast<const Raw*>(in + at[u].b + (int64_t)head * a.D);
+        }
+      }
+      float r[kHeads];
+      if constexpr (kNorm) {
+        float ss[kHeads];
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+          ss[k] = 0.f;
+#pragma unroll
+          for (int u = 0; u < kUnits; ++u) {
+            const F4 x = Four<T>::get(ra[k][u]), y = Four<T>::get(rb[k][u]);
+            const float v = sum4(fma4(y, y, mul4(x, x)));
+            ss[k] += at[u].on ? v : 0.f;
           }
         }
+        for (int o = w.lanes >> 1; o; o >>= 1)
+#pragma unroll
+          for (int k = 0; k < kHeads; ++k) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) r[k] = rsqrtf(ss[k] / a.D + a.eps);
       }
 #pragma unroll
       for (int k = 0; k < kHeads; ++k) {
-        T* to_head = out + ((step + k) * groups + group) * a.D;
-        Pairs p[kUnits];
-#pragma unroll
-        for (int u = 0; u < kUnits; ++u) p[u] = as_pairs<kInter>(Four<T>::get(ra[k][u]), Four<T>::get(rb[k][u]));
-        if constexpr (kNorm) {
-          F4 ss = all4(0.f);
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) ss = dot4(p[u], p[u], ss);
-          const float r = rsqrtf(group_sum(sum4(ss), w.lanes) / a.D + a.eps);
-#pragma unroll
-          for (int u = 0; u < kUnits; ++u) p[u] = times(scaled(p[u], r), weight[u]);
-        }
+        const int head = (step + k) * groups + group;
+        if (step + k >= to || head >= t.H) continue;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          if (!there[k] || !at[u].on) continue;
-          if (at[u].turned) p[u] = rotate(p[u], turn[u]);
+          if (!at[u].on) continue;
+          T* const oa = out + at[u].a + (int64_t)head * a.D;
+          T* const ob = out + at[u].b + (int64_t)head * a.D;
+          if (!kNorm && !at[u].turned) {  // a copy
+            *reinterpret_cast<Raw*>(oa) = ra[k][u];
+            *reinterpret_cast<Raw*>(ob) = rb[k][u];
+            continue;
+          }
+          Pairs p = as_pairs<kInter>(Four<T>::get(ra[k][u]), Four<T>::get(rb[k][u]));
+          if constexpr (kNorm) p = scaled(p, r[k]);
+          p = at[u].turned ? mix(p, turn[u]) : Pairs{mul4(p.x, turn[u].xc), mul4(p.y, turn[u].yc)};
           F4 x, y;
-          as_quads<kInter>(p[u], x, y);
-          Raw oa = Four<T>::put(x), ob = Four<T>::put(y);
-          if (!kNorm && !at[u].turned) oa = ra[k][u], ob = rb[k][u];  // a copy
-          *reinterpret_cast<Raw*>(to_head + at[u].a) = oa;
-          *reinterpret_cast<Raw*>(to_head + at[u].b) = ob;
+          as_quads<kInter>(p, x, y);
+          store4(oa, x);
+          store4(ob, y);
         }
       }
     }
@@ -211,7 +237,8 @@ __global__ void __launch_bounds__(kThreads) qk_rope_k(QkRopeArgs a, Split w) {
 // Warps walk the items with a stride and keep the weight gradients of their lanes' channels;
 // a block adds its groups and warps in a fixed order and writes one row for q and one for k.
 template <typename T, bool kInter, int kUnits>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
+__global__ void __launch_bounds__(kThreads, kUnits == 1 ? 5 : 3) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
+  using Raw = typename Four<T>::Raw;
   __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
   __shared__ __align__(16) float sums[kWarps][2][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -225,65 +252,70 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_bwd_k(QkRopeArgs a, Spl
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int u = 0; u < kUnits; ++u) dw[i][u] = Pairs{all4(0.f), all4(0.f)};
-  const int steps = w.q_steps + w.k_steps;
   for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < w.items; item += (int64_t)gridDim.x * kWarps) {
     const int64_t row = w.parts == 1 ? item : item / w.parts;
     const int part = (int)(item - row * w.parts);
     __syncwarp();  // the angles of the item before have been read
     angles(a, row, cs[warp]);
     __syncwarp();
-    Turn turn[kUnits];
+    Mix back[kUnits];
 #pragma unroll
     for (int u = 0; u < kUnits; ++u)
-      if (at[u].turned) turn[u] = turn_of(cs[warp] + 4 * (u * w.lanes + within));
-    const int first = (int)((int64_t)steps * part / w.parts), last = (int)((int64_t)steps * (part + 1) / w.parts);
+      if (at[u].turned) {
+        const Turn f = turn_of(cs[warp] + 4 * min(u * w.lanes + within, a.D / 8 - 1));
+        back[u] = Mix{f.c, minus(f.s), f.c, f.s};
+      }
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const HeadRows& t = which ? a.k : a.q;
-      const int from = which ? max(first - w.q_steps, 0) : first, to = which ? last - w.q_steps : min(last, w.q_steps);
+      int from, to;
+      share(w, part, which, from, to);
       if (from >= to) continue;
       const T* in = static_cast<const T*>(t.in) + row * t.stride;
       const T* grad = static_cast<const T*>(t.grad) + row * t.grad_stride;
       T* out = static_cast<T*>(t.out) + row * t.out_stride;
-      Pairs weight[kUnits];
-#pragma unroll
-      for (int u = 0; u < kUnits; ++u)
-        if (at[u].on) weight[u] = as_pairs<kInter>(load4(t.weight + at[u].a), load4(t.weight + at[u].b));
-#pragma unroll 2
+#pragma unroll 1
       for (int step = from; step < to; ++step) {
         const int head = step * groups + group;
-        const bool there = head < t.H;
-        Pairs x[kUnits], g[kUnits];
+        const int64_t off = (int64_t)min(head, t.H - 1) * a.D;
+        Raw xa[kUnits], xb[kUnits], ga[kUnits], gb[kUnits];
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          x[u] = g[u] = Pairs{all4(0.f), all4(0.f)};
-          if (there && at[u].on) {
-            x[u] = as_pairs<kInter>(load4(in + head * a.D + at[u].a), load4(in + head * a.D + at[u].b));
-            g[u] = as_pairs<kInter>(load4(grad + head * a.D + at[u].a), load4(grad + head * a.D + at[u].b));
-          }
+          xa[u] = *reinterpret_cast<const Raw*>(in + at[u].a + off);
+          xb[u] = *reinterpret_cast<const Raw*>(in + at[u].b + off);
+          ga[u] = *reinterpret_cast<const Raw*>(grad + at[u].a + off);
+          gb[u] = *reinterpret_cast<const Raw*>(grad + at[u].b + off);
         }
-        F4 ss = all4(0.f), dot = all4(0.f);
-        Pairs wg[kUnits];
+        float ss = 0.f, dot = 0.f;
+        Pairs g[kUnits], wg[kUnits];
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          if (at[u].turned) g[u] = rotate_back(g[u], turn[u]);
-          wg[u] = at[u].on ? times(g[u], weight[u]) : g[u];
-          ss = dot4(x[u], x[u], ss);
-          dot = dot4(x[u], wg[u], dot);
+          const Pairs x = as_pairs<kInter>(Four<T>::get(xa[u]), Four<T>::get(xb[u]));
+          g[u] = as_pairs<kInter>(Four<T>::get(ga[u]), Four<T>::get(gb[u]));
+          if (at[u].turned) g[u] = mix(g[u], back[u]);
+          wg[u] = times(g[u], as_pairs<kInter>(load4(t.weight + at[u].a), load4(t.weight + at[u].b)));
+          const float s = sum4(fma4(x.y, x.y, mul4(x.x, x.x))), d = sum4(fma4(x.y, wg[u].y, mul4(x.x, wg[u].x)));
+          ss += at[u].on ? s : 0.f;
+          dot += at[u].on ? d : 0.f;
         }
-        const float r = rsqrtf(group_sum(sum4(ss), w.lanes) * inv_d + a.eps);
-        const float m = group_sum(sum4(dot), w.lanes) * r * inv_d;
+        for (int o = w.lanes >> 1; o; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        }
+        const float r = rsqrtf(ss * inv_d + a.eps);
+        const float m = dot * r * inv_d;
+        if (head >= t.H) continue;
 #pragma unroll
         for (int u = 0; u < kUnits; ++u) {
-          if (!there || !at[u].on) continue;
-          const Pairs n = scaled(x[u], r);
+          if (!at[u].on) continue;
+          const Pairs n = scaled(as_pairs<kInter>(Four<T>::get(xa[u]), Four<T>::get(xb[u])), r);
           dw[which][u] = Pairs{fma4(g[u].x, n.x, dw[which][u].x), fma4(g[u].y, n.y, dw[which][u].y)};
           Pairs d{fma4(n.x, all4(-m), wg[u].x), fma4(n.y, all4(-m), wg[u].y)};
           d = scaled(d, r);
           F4 p, q;
           as_quads<kInter>(d, p, q);
-          store4(out + head * a.D + at[u].a, p);
-          store4(out + head * a.D + at[u].b, q);
+          store4(out + at[u].a + off, p);
+          store4(out + at[u].b + off, q);
         }
       }
     }

@@ -188,20 +188,31 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
   const long long pos = position(a, row);
   const Lane<kInter> at(a, w.lanes);
   Raw ra[kHeads], rb[kHeads];
-  auto load = [&](const HeadRows& t, int step) {
-    const T* in = static_cast<const T*>(t.in) + row * t.stride;
+  const int to_b = at.b - at.a, next = at.groups * a.D;  // from quad to quad, from step to step
+  const T* in;
+  int head, end;  // this lane's head, and what it is below
+  auto start = [&](const HeadRows& t, int from, int to) {
+    head = from * at.groups + at.group;
+    end = at.on ? min(to * at.groups, t.H) : 0;
+    in = static_cast<const T*>(t.in) + row * t.stride + (int64_t)head * a.D + at.a;
+  };
+  auto load = [&] {
 #pragma unroll
     for (int k = 0; k < kHeads; ++k) {
-      const T* head = in + (int64_t)min((step + k) * at.groups + at.group, t.H - 1) * a.D;
-      ra[k] = *reinterpret_cast<const Raw*>(head + at.a);
-      rb[k] = *reinterpret_cast<const Raw*>(head + at.b);
+      ra[k] = rb[k] = Raw{};
+      if (head + k * at.groups < end) {
+        ra[k] = *reinterpret_cast<const Raw*>(in + k * next);
+        rb[k] = *reinterpret_cast<const Raw*>(in + k * next + to_b);
+      }
     }
+    in += kHeads * next;
   };
   int from, to;
   share(w, part, 0, from, to);
   int which = from < to ? 0 : 1;  // the share may lie in k alone
   if (which) share(w, part, 1, from, to);
-  load(which ? a.k : a.q, from);  // the first heads travel while the angles are computed
+  start(which ? a.k : a.q, from, to);
+  load();  // the first heads travel while the angles are computed
   angles(a, pos, cs[warp]);
   __syncwarp();
 #pragma unroll 1
@@ -209,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
     const HeadRows& t = which ? a.k : a.q;
     share(w, part, which, from, to);
     if (from >= to) continue;
-    T* out = static_cast<T*>(t.out) + row * t.out_stride;
+    if (!loaded) start(t, from, to);
+    T* out = static_cast<T*>(t.out) + row * t.out_stride + (int64_t)head * a.D + at.a;
     Mix turn{all4(1.f), all4(0.f), all4(1.f), all4(0.f)};  // xc, yc: the weights alone where nothing turns
     if (at.turned) {
       const Turn f = turn_of(cs[warp] + at.pair);
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
     }
 #pragma unroll 1
     for (int step = from; step < to; step += kHeads) {
-      if (!loaded) load(t, step);
+      if (!loaded) load();
       loaded = false;
       float r[kHeads];
       if constexpr (kNorm) {
@@ -238,12 +250,11 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
       }
 #pragma unroll
       for (int k = 0; k < kHeads; ++k) {
-        const int head = (step + k) * at.groups + at.group;
-        if (step + k >= to || head >= t.H || !at.on) continue;
-        T* const to_head = out + (int64_t)head * a.D;
+        if (head + k * at.groups >= end) continue;
+        T* const oa = out + k * next;
         if (!kNorm && !at.turned) {  // a copy
-          *reinterpret_cast<Raw*>(to_head + at.a) = ra[k];
-          *reinterpret_cast<Raw*>(to_head + at.b) = rb[k];
+          *reinterpret_cast<Raw*>(oa) = ra[k];
+          *reinterpret_cast<Raw*>(oa + to_b) = rb[k];
           continue;
         }
         Pairs p = as_pairs<kInter>(Four<T>::get(ra[k]), Four<T>::get(rb[k]));
@@ -251,9 +262,11 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
         p = at.turned ? mix(p, turn) : Pairs{mul4(p.x, turn.xc), mul4(p.y, turn.yc)};
         F4 x, y;
         as_quads<kInter>(p, x, y);
-        store4(to_head + at.a, x);
-        store4(to_head + at.b, y);
+        store4(oa, x);
+        store4(oa + to_b, y);
       }
+      head += kHeads * at.groups;
+      out += kHeads * next;
     }
   }
 }
@@ -262,37 +275,24 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
 // Warps walk the items with a stride and keep the weight gradients of their lanes' channels;
 // a block adds its groups and warps in a fixed order and writes one row for q and one for k.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads, 6) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
+__global__ void __launch_bounds__(kThreads, 5) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
   using Raw = typename Four<T>::Raw;
+  constexpr int kHeads = 2;  // in flight
   __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
   __shared__ __align__(16) float sums[kWarps][2][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const float inv_d = 1.f / a.D;
   const Lane<kInter> at(a, w.lanes);
   Pairs dw[2] = {Pairs{all4(0.f), all4(0.f)}, Pairs{all4(0.f), all4(0.f)}};
-  Raw xa, xb, ga, gb;
-  auto load = [&](const HeadRows& t, int64_t row, int step) {
-    const int64_t off = (int64_t)min(step * at.groups + at.group, t.H - 1) * a.D;
-    const T* in = static_cast<const T*>(t.in) + row * t.stride + off;
-    const T* grad = static_cast<const T*>(t.grad) + row * t.grad_stride + off;
-    xa = *reinterpret_cast<const Raw*>(in + at.a);
-    xb = *reinterpret_cast<const Raw*>(in + at.b);
-    ga = *reinterpret_cast<const Raw*>(grad + at.a);
-    gb = *reinterpret_cast<const Raw*>(grad + at.b);
-  };
   auto row_of = [&](int64_t item) { return w.parts == 1 ? item : item / w.parts; };
   const int64_t stride = (int64_t)gridDim.x * kWarps;
+  const int to_b = at.b - at.a, next = at.groups * a.D;  // from quad to quad, from step to step
   int64_t item = (int64_t)blockIdx.x * kWarps + warp;
   long long pos = item < w.items ? position(a, row_of(item)) : 0;
   for (; item < w.items; item += stride) {
     const int64_t row = row_of(item);
     const int part = (int)(item - row * w.parts);
-    int from, to;
-    share(w, part, 0, from, to);
-    const bool in_q = from < to;
-    if (!in_q) share(w, part, 1, from, to);
-    load(in_q ? a.q : a.k, row, from);  // the first heads travel while the angles are computed
-    __syncwarp();                       // the angles of the item before have been read
+    __syncwarp();  // the angles of the item before have been read
     angles(a, pos, cs[warp]);
     if (item + stride < w.items) pos = position(a, row_of(item + stride));
     __syncwarp();
@@ -304,38 +304,65 @@ __global__ void __launch_bounds__(kThreads, 6) qk_norm_rope_bwd_k(QkRopeArgs a, 
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
       const HeadRows& t = which ? a.k : a.q;
+      int from, to;
       share(w, part, which, from, to);
       if (from >= to) continue;
-      T* out = static_cast<T*>(t.out) + row * t.out_stride;
       const Pairs weight = as_pairs<kInter>(load4(t.weight + at.a), load4(t.weight + at.b));
+      int head = from * at.groups + at.group;
+      const int64_t off = (int64_t)head * a.D + at.a;
+      const T* in = static_cast<const T*>(t.in) + row * t.stride + off;
+      const T* grad = static_cast<const T*>(t.grad) + row * t.grad_stride + off;
+      T* out = static_cast<T*>(t.out) + row * t.out_stride + off;
+      const int end = at.on ? min(to * at.groups, t.H) : 0;  // this lane's heads are below it
 #pragma unroll 1
-      for (int step = from; step < to; ++step) {
-        const int head = step * at.groups + at.group;
-        const Pairs x = as_pairs<kInter>(Four<T>::get(xa), Four<T>::get(xb));
-        Pairs g = as_pairs<kInter>(Four<T>::get(ga), Four<T>::get(gb));
-        // The next heads of the share.
-        if (step + 1 < to)
-          load(t, row, step + 1);
-        else if (which == 0) {
-          share(w, part, 1, from, to);
-          if (from < to) load(a.k, row, from);
-          from = to = 0;  // leaves this loop
+      for (int step = from; step < to; step += kHeads) {
+        Raw xa[kHeads], xb[kHeads], ga[kHeads], gb[kHeads];
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+          xa[k] = xb[k] = ga[k] = gb[k] = Raw{};
+          if (head + k * at.groups < end) {
+            xa[k] = *reinterpret_cast<const Raw*>(in + k * next);
+            xb[k] = *reinterpret_cast<const Raw*>(in + k * next + to_b);
+            ga[k] = *reinterpret_cast<const Raw*>(grad + k * next);
+            gb[k] = *reinterpret_cast<const Raw*>(grad + k * next + to_b);
+          }
         }
-        if (at.turned) g = mix(g, back);
-        const Pairs wg = times(g, weight);
-        float sd[2] = {sum4(fma4(x.y, x.y, mul4(x.x, x.x))), sum4(fma4(x.y, wg.y, mul4(x.x, wg.x)))};
+        float sd[2 * kHeads];
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+          const Pairs x = as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k]));
+          Pairs g = as_pairs<kInter>(Four<T>::get(ga[k]), Four<T>::get(gb[k]));
+          if (at.turned) g = mix(g, back);
+          const Pairs wx = times(x, weight);
+          sd[2 * k] = sum4(fma4(x.y, x.y, mul4(x.x, x.x)));
+          sd[2 * k + 1] = sum4(fma4(wx.y, g.y, mul4(wx.x, g.x)));
+          xa[k] = again(xa[k]);
+          xb[k] = again(xb[k]);
+          ga[k] = again(ga[k]);
+          gb[k] = again(gb[k]);
+        }
         group_sum(sd, at.g);
-        const float r = rsqrtf(sd[0] * inv_d + a.eps);
-        const float m = sd[1] * r * inv_d;
-        if (head >= t.H || !at.on) continue;
-        const Pairs n = scaled(x, r);
-        dw[which] = Pairs{fma4(g.x, n.x, dw[which].x), fma4(g.y, n.y, dw[which].y)};
-        const Pairs d = scaled(Pairs{fma4(n.x, all4(-m), wg.x), fma4(n.y, all4(-m), wg.y)}, r);
-        F4 p, q;
-        as_quads<kInter>(d, p, q);
-        T* const to_head = out + (int64_t)head * a.D;
-        store4(to_head + at.a, p);
-        store4(to_head + at.b, q);
+#pragma unroll
+        for (int k = 0; k < kHeads; ++k) {
+          if (head + k * at.groups >= end) continue;
+          const float r = rsqrtf(sd[2 * k] * inv_d + a.eps);
+          const float m = sd[2 * k + 1] * r * inv_d;
+          Pairs g = as_pairs<kInter>(Four<T>::get(ga[k]), Four<T>::get(gb[k]));
+          if (at.turned) g = mix(g, back);
+          const Pairs n = scaled(as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k])), r);
+          dw[which] = Pairs{fma4(g.x, n.x, dw[which].x), fma4(g.y, n.y, dw[which].y)};
+          // r (w g - m n)
+          const Pairs wg = times(scaled(g, r), weight);
+          const F4 mr = all4(-m * r);
+          F4 p, q;
+          as_quads<kInter>(Pairs{fma4(n.x, mr, wg.x), fma4(n.y, mr, wg.y)}, p, q);
+          store4(out + k * next, p);
+          store4(out + k * next + to_b, q);
+        }
+        head += kHeads * at.groups;
+        in += kHeads * next;
+        grad += kHeads * next;
+        out += kHeads * next;
       }
     }
   }
@@ -405,7 +432,7 @@ cudaError_t forward(const QkRopeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-constexpr int kBwdBlocks = 148 * 6;
+constexpr int kBwdBlocks = 148 * 5;
 int bwd_blocks(const Split& w) { return (int)std::min<int64_t>(kBwdBlocks, (w.items + kWarps - 1) / kWarps); }
 
 template <typename T>

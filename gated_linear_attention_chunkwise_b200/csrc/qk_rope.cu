@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
 // Warps walk the items with a stride and keep the weight gradients of their lanes' channels;
 // a block adds its groups and warps in a fixed order and writes one row for q and one for k.
 template <typename T, bool kInter>
-__global__ void __launch_bounds__(kThreads, 5) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
   using Raw = typename Four<T>::Raw;
   constexpr int kHeads = 2;  // in flight
   __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
@@ -432,7 +432,7 @@ cudaError_t forward(const QkRopeArgs& a, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-constexpr int kBwdBlocks = 148 * 5;
+constexpr int kBwdBlocks = 148 * 4;
 int bwd_blocks(const Split& w) { return (int)std::min<int64_t>(kBwdBlocks, (w.items + kWarps - 1) / kWarps); }
 
 template <typename T>

@@ -81,13 +81,14 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
 
   bool grown = false;
   Amid amid;
-  Marks next{0u, 0u, 0u};
+  Marks next;
   F4 next_entry = all4(0.f);
   auto look = [&](int from) {
     // Backwards over sequences in token order the token falls by one each step.
     const int n = on ? max(0, min(kRun, g.T - from)) : 0;
     next = mark(a, a.dir ? from : g.T - from - n, n, a.dir == 0, amid);
-    next_entry = entering(a, a.dh_last, next.last, a.dir ? from : g.T - 1 - from, a.dir ? 1 : -1, c);
+    // Fetched a round ahead: a thread that waited for it would hold up its whole cluster.
+    if (next.last && a.dh_last) next_entry = load4(a.dh_last + (int64_t)next.last_seq * a.C + c);
   };
   if (packed) look(j0);
   for (int round = 0; round < rounds; ++round, j0 += per_round) {
@@ -109,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
         before = all4(0.f);
         if (a.h0) {
           Rows rows(g, g.T - 1 - (j0 + i), -1);
-          before = load4(a.h0 + (packed ? state_row(a, rows.next(g)) : (int64_t)b * a.C) + c);
+          const int row = rows.next(g);
+          before = load4(a.h0 + (packed ? state_row(a, m.first, i, m.first_seq, row) : (int64_t)b * a.C) + c);
         }
       }
       if constexpr (kComp) {
@@ -134,7 +136,9 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
         const int row = i < n ? rows.next(g) : 0;
         if (m.last >> i & 1u) {
           if (a.dh_last)
-            d[i] = add4(d[i], m.last & ((1u << i) - 1u) ? load4(a.dh_last + state_row(a, row) + c) : entry);
+            d[i] = add4(d[i], m.last & ((1u << i) - 1u)
+                                  ? load4(a.dh_last + state_row(a, m.last, i, m.last_seq, row) + c)
+                                  : entry);
           s = Span{all4(1.f), mul4(al[i], d[i])};
         } else {
           s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), mul4(al[i], add4(d[i], s.h))};
@@ -173,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
         const int64_t row = rows.next(g);
         const F4 delta = m.last >> i & 1u ? d[i] : add4(d[i], r);
         r = mul4(al[i], delta);
-        if (packed && a.dh0 && (m.first >> i & 1u)) store4(a.dh0 + state_row(a, (int)row) + c, r);
+        if (packed && a.dh0 && (m.first >> i & 1u)) store4(a.dh0 + state_row(a, m.first, i, m.first_seq, (int)row) + c, r);
         F4 vx = kComp ? mul4(delta, keep[kComp ? i : 0]) : delta, vg = mul4(r, pull[i]);
         if (packed && !(m.inside >> i & 1u)) {
           if (!a.fill) continue;

@@ -66,12 +66,13 @@ __global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3)
 
   bool grown = false;
   Amid amid;
-  Marks next{0u, 0u, 0u};
+  Marks next;
   F4 next_entry = all4(0.f);
   auto look = [&](int from) {
     const int n = on ? max(0, min(kRun, g.T - from)) : 0;
     next = mark(a, a.dir ? g.T - from - n : from, n, a.dir != 0, amid);
-    next_entry = entering(a, a.h0, next.first, a.dir ? g.T - 1 - from : from, a.dir ? -1 : 1, c);
+    // Fetched a round ahead: a thread that waited for it would hold up its whole cluster.
+    if (next.first && a.h0) next_entry = load4(a.h0 + (int64_t)next.first_seq * a.C + c);
   };
   if (packed) look(p0);
   for (int round = 0; round < rounds; ++round, p0 += per_round) {
@@ -104,7 +105,9 @@ __global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3)
         const int row = i < n ? rows.next(g) : 0;
         if (m.first >> i & 1u) {
           if (a.h0)
-            u[i] = fma4(al[i], m.first & ((1u << i) - 1u) ? load4(a.h0 + state_row(a, row) + c) : entry, u[i]);
+            u[i] = fma4(al[i],
+                        m.first & ((1u << i) - 1u) ? load4(a.h0 + state_row(a, m.first, i, m.first_seq, row) + c) : entry,
+                        u[i]);
           s = Span{all4(1.f), u[i]};
         } else {
           s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), fma4(al[i], s.h, u[i])};
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3)
           store4(out + (int64_t)row * a.C, h);
         else if (a.fill)
           store4(out + (int64_t)row * a.C, all4(0.f));
-        if (a.h_last && (m.last >> i & 1u)) store4(a.h_last + state_row(a, row) + c, h);
+        if (a.h_last && (m.last >> i & 1u)) store4(a.h_last + state_row(a, m.last, i, m.last_seq, row) + c, h);
       }
     }
   }

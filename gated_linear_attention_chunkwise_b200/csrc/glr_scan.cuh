@@ -284,8 +284,25 @@ __device__ __forceinline__ void fetch(uint32_t slot, const T* p, bool there) {
 // ---- packed sequences ---------------------------------------------------------------------------
 
 // Sequence of packed token t: the last n in [0, nseq) with cu[n] <= t, or -1 before all.
-__device__ __forceinline__ int find_sequence(const int* cu, int nseq, int t) {
-  int lo = 0, hi = nseq;
+// near: a sequence that a token near t lay in; the search widens from there.
+__device__ __forceinline__ int find_sequence(const int* cu, int nseq, int t, int near) {
+  int lo = min(max(near, 0), nseq - 1), hi, step = 1;  // then cu[lo - 1] <= t < cu[hi] where they exist
+  if (cu[lo] <= t) {
+    hi = ++lo;
+    while (hi < nseq && cu[hi] <= t) {
+      lo = hi + 1;
+      hi = min(hi + step, nseq);
+      step *= 2;
+    }
+    lo = min(lo, hi);
+  } else {
+    hi = lo;
+    while (lo > 0 && cu[lo - 1] > t) {
+      hi = lo - 1;
+      lo = max(lo - step, 0);
+      step *= 2;
+    }
+  }
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
     if (cu[mid] <= t)
@@ -295,49 +312,55 @@ __device__ __forceinline__ int find_sequence(const int* cu, int nseq, int t) {
   }
   return lo - 1;
 }
-// Its row in the states, for a token that mark() found to begin or end a sequence (in range
-// whatever the lengths hold).
-__device__ __forceinline__ int64_t state_row(const GlrArgs& a, int t) {
-  return (int64_t)max(find_sequence(a.cu, a.nseq, t), 0) * a.C;
-}
-
-// The state h0 or dh_last that enters at the first marked token, fetched a round ahead: a
-// thread that waited for it would hold up its whole cluster.
-__device__ __forceinline__ F4 entering(const GlrArgs& a, const float* states, uint32_t marks, int token0, int by, int c) {
-  if (!states || marks == 0u) return all4(0.f);
-  return load4(states + state_row(a, token0 + by * (__ffs(marks) - 1)) + c);
-}
 
 // Of a thread's tokens (bit i: the i-th it walks): which lie in a sequence, begin one, end
 // one (first and last in scan order).
 struct Marks {
-  uint32_t inside, first, last;
+  uint32_t inside = 0u, first = 0u, last = 0u;
+  int first_seq = 0, last_seq = 0;  // the sequences of the lowest such bits
 };
 // The sequence a thread was last amid: tokens strictly between its ends need no search.
 struct Amid {
-  int begin = 0, end = 0;
+  int begin = 0, end = 0, n = 0;
 };
 // The tokens are lo .. lo + n - 1; turned: walked from the highest to the lowest.
 __device__ __forceinline__ Marks mark(const GlrArgs& a, int lo, int n, bool turned, Amid& at) {
-  Marks m{(1u << n) - 1u, 0u, 0u};
+  Marks m;
+  m.inside = (1u << n) - 1u;
   if (n <= 0 || (lo > at.begin && lo + n < at.end)) return m;
-  int q = find_sequence(a.cu, a.nseq, lo);
-  if (q >= 0) {
-    at = Amid{a.cu[q], a.cu[q + 1]};
-    if (lo > at.begin && lo + n < at.end) return m;
-  }
+  int q = find_sequence(a.cu, a.nseq, lo, at.n);
+  const int end = lo + n;
   m.inside = 0u;
-  for (int i = 0; i < n; ++i) {
-    const int t = lo + i;
-    while (q + 1 < a.nseq && a.cu[q + 1] <= t) ++q;
-    if (q < 0 || t >= a.cu[q + 1]) continue;
-    const uint32_t bit = 1u << (turned ? n - 1 - i : i);
-    m.inside |= bit;
-    const bool lowest = t == a.cu[q], highest = t + 1 == a.cu[q + 1];
-    if (a.dir ? highest : lowest) m.first |= bit;
-    if (a.dir ? lowest : highest) m.last |= bit;
+  int s = q < 0 ? 0 : a.cu[q], e = q < 0 ? a.cu[0] : a.cu[q + 1];
+  at = Amid{s, e, q};
+  while (true) {  // one sequence after another
+    const int from = max(s, lo), to = min(e, end);
+    if (q >= 0 && from < to) {
+      uint32_t bits = ((1u << (to - from)) - 1u) << (from - lo), low = s >= lo ? 1u << (s - lo) : 0u,
+               high = e <= end ? 1u << (e - 1 - lo) : 0u;
+      if (turned) {
+        bits = __brev(bits) >> (32 - n);
+        low = __brev(low) >> (32 - n);
+        high = __brev(high) >> (32 - n);
+      }
+      const uint32_t first = a.dir ? high : low, last = a.dir ? low : high;
+      m.inside |= bits;
+      if (first && (m.first == 0u || first < (m.first & (0u - m.first)))) m.first_seq = q;
+      if (last && (m.last == 0u || last < (m.last & (0u - m.last)))) m.last_seq = q;
+      m.first |= first;
+      m.last |= last;
+    }
+    if (e >= end || ++q >= a.nseq) break;
+    s = e;
+    e = a.cu[q + 1];
   }
   return m;
+}
+// The row in the states of the sequence that token t begins or ends, marked as bit i of
+// `marks` whose lowest bit is in sequence `known` (in range whatever the lengths hold).
+__device__ __forceinline__ int64_t state_row(const GlrArgs& a, uint32_t marks, int i, int known, int t) {
+  const int n = marks & ((1u << i) - 1u) ? max(find_sequence(a.cu, a.nseq, t, known), 0) : known;
+  return (int64_t)n * a.C;
 }
 
 // States of sequences of no token, which no thread reaches through its tokens, and the check

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
     cp_async_wait_all();
     // pull = (h before - [complement] x) d log_alpha / d gate, keep = 1 - alpha.
     F4 al[kRun], d[kRun], pull[kRun], keep[kComp ? kRun : 1];
-    Span s = nothing();
+    auto token = [&](int i) { return a.dir ? j0 + i : g.T - 1 - (j0 + i); };  // of packed rows
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
@@ -108,45 +108,48 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
       al[i] = k.alpha;
       if (m.first >> i & 1u) {
         before = all4(0.f);
-        if (a.h0) {
-          Rows rows(g, g.T - 1 - (j0 + i), -1);
-          const int row = rows.next(g);
-          before = load4(a.h0 + (packed ? state_row(a, m.first, i, m.first_seq, row) : (int64_t)b * a.C) + c);
-        }
+        if (a.h0)
+          before = load4(a.h0 + (packed ? state_row(a, m.first, i, m.first_seq, token(i)) : (int64_t)b * a.C) + c);
       }
       if constexpr (kComp) {
         before = sub4(before, Four<T>::get(sx[i * kThreads]));
         keep[i] = k.rest;
       }
       pull[i] = kKind == kGateLog ? before : mul4(before, k.slope);
-      s = i == 0 ? Span{al[0], mul4(al[0], d[0])} : Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
     }
-    // Tokens that are missing or end a sequence, growth, and NaN gates are folded again.
-    const bool plain = n == kRun && m.last == 0u;
-    bool odd = !all_within(s.A, 1.f);
-    if (!plain || odd) {
+    // The last token of a sequence takes dh_last in and forgets the token behind.
+    Span s = nothing();
+    if (m.last) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (m.last >> i & 1u) {
+          F4 from = entry;
+          if (a.dh_last && (m.last & ((1u << i) - 1u)))
+            from = load4(a.dh_last + state_row(a, m.last, i, m.last_seq, token(i)) + c);
+          d[i] = add4(d[i], from);
+          s = Span{all4(0.f), all4(0.f)};
+        }
+        s = Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) s = Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
+    }
+    bool odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
+    if (n < kRun || odd) {  // the last round's end, growth, values that are not finite
       s = nothing();
-      Rows rows(g, g.T - 1 - j0, -1);
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         if (i >= n) {
           al[i] = all4(1.f);
           d[i] = all4(0.f);
         }
-        const int row = i < n ? rows.next(g) : 0;
-        if (m.last >> i & 1u) {
-          if (a.dh_last)
-            d[i] = add4(d[i], m.last & ((1u << i) - 1u)
-                                  ? load4(a.dh_last + state_row(a, m.last, i, m.last_seq, row) + c)
-                                  : entry);
-          s = Span{all4(1.f), mul4(al[i], d[i])};
-        } else {
-          s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), mul4(al[i], add4(d[i], s.h))};
-        }
+        if (m.last >> i & 1u) s = Span{all4(0.f), all4(0.f)};
+        s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), mul4(al[i], add4(d[i], s.h))};
       }
-      odd = m.last != 0u || !all_within(s.A, 1.f);
-      if (m.last) s.A.a.x = -0.f;
+      odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
     }
+    if (m.last) s.A.a.x = -0.f;
     F4 r;
     const bool going = walk.exchange(s, odd, packed, round, r, grown, [&] {
       if (round + 1 < rounds) {
@@ -157,10 +160,23 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
     if (!going) break;
     Rows rows(g, g.T - 1 - j0, -1);
     int apart;
-    if (plain && (!packed || m.first == 0u) && rows.even(g, kRun, apart) && (!packed || m.inside == (1u << kRun) - 1u)) {
-      const int64_t row = rows.next(g), step = (int64_t)apart * a.C;
-      T* px = dx + row * a.C;
-      G* pg = dgate + row * a.C;
+    if (!rows.even(g, kRun, apart)) {  // grids alone
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        const F4 delta = add4(d[i], r);
+        r = mul4(al[i], delta);
+        if (i >= n) continue;
+        const int64_t row = rows.next(g);
+        store4(dx + row * a.C, kComp ? mul4(delta, keep[kComp ? i : 0]) : delta);
+        store4(dgate + row * a.C, mul4(r, pull[i]));
+      }
+      continue;
+    }
+    const uint32_t write = packed ? m.inside : (1u << n) - 1u;
+    const int64_t row = rows.next(g), step = (int64_t)apart * a.C;
+    T* px = dx + row * a.C;
+    G* pg = dgate + row * a.C;
+    if (write == (1u << kRun) - 1u && (!packed || (m.first | m.last) == 0u)) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         const F4 delta = add4(d[i], r);
@@ -170,22 +186,23 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
         px += step;
         pg += step;
       }
-    } else {
+      continue;
+    }
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        if (i >= n) break;
-        const int64_t row = rows.next(g);
-        const F4 delta = m.last >> i & 1u ? d[i] : add4(d[i], r);
-        r = mul4(al[i], delta);
-        if (packed && a.dh0 && (m.first >> i & 1u)) store4(a.dh0 + state_row(a, m.first, i, m.first_seq, (int)row) + c, r);
-        F4 vx = kComp ? mul4(delta, keep[kComp ? i : 0]) : delta, vg = mul4(r, pull[i]);
-        if (packed && !(m.inside >> i & 1u)) {
-          if (!a.fill) continue;
-          vx = vg = all4(0.f);
-        }
-        store4(dx + row * a.C, vx);
-        store4(dgate + row * a.C, vg);
+    for (int i = 0; i < kRun; ++i) {
+      const F4 delta = m.last >> i & 1u ? d[i] : add4(d[i], r);
+      r = mul4(al[i], delta);
+      if (packed && a.dh0 && (m.first >> i & 1u))
+        store4(a.dh0 + state_row(a, m.first, i, m.first_seq, token(i)) + c, r);
+      if (write >> i & 1u) {
+        store4(px, kComp ? mul4(delta, keep[kComp ? i : 0]) : delta);
+        store4(pg, mul4(r, pull[i]));
+      } else if (a.fill && i < n) {
+        store4(px, all4(0.f));
+        store4(pg, all4(0.f));
       }
+      px += step;
+      pg += step;
     }
   }
   cp_async_wait_all();

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3)
   bool grown = false;
   Amid amid;
   Marks next;
-  F4 next_entry = all4(0.f);
+  F4 next_entry = all4(0.f);  // stays zero without h0
   auto look = [&](int from) {
     const int n = on ? max(0, min(kRun, g.T - from)) : 0;
     next = mark(a, a.dir ? g.T - from - n : from, n, a.dir != 0, amid);
@@ -81,41 +81,45 @@ __global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3)
     const F4 entry = next_entry;
     cp_async_wait_all();
     F4 al[kRun], u[kRun];
-    Span s = nothing();
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
       const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
       u[i] = Four<T>::get(sx[i * kThreads]);
       if constexpr (kComp) u[i] = mul4(k.rest, u[i]);
       al[i] = k.alpha;
-      s = i == 0 ? Span{al[0], u[0]} : Span{mul4(s.A, al[i]), fma4(al[i], s.h, u[i])};
     }
-    // Tokens that are missing or begin a sequence, growth, and NaN gates are folded again.
-    const bool plain = n == kRun && m.first == 0u;
-    bool odd = !all_within(s.A, 1.f);
-    if (!plain || odd) {
+    // The first token of a sequence takes its state in and forgets the token before.
+    if (m.first) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (!(m.first >> i & 1u)) continue;
+        F4 from = entry;
+        if (a.h0 && (m.first & ((1u << i) - 1u)))
+          from = load4(a.h0 + state_row(a, m.first, i, m.first_seq, a.dir ? g.T - 1 - (p0 + i) : p0 + i) + c);
+        u[i] = fma4(al[i], from, u[i]);
+        al[i] = all4(0.f);
+      }
+    }
+    Span s{al[0], u[0]};
+#pragma unroll
+    for (int i = 1; i < kRun; ++i) s = Span{mul4(s.A, al[i]), fma4(al[i], s.h, u[i])};
+    bool odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
+    if (n < kRun || odd) {  // the last round's end, growth, values that are not finite
       s = nothing();
-      Rows rows(g, p0, 1);
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         if (i >= n) {
           al[i] = all4(1.f);
           u[i] = all4(0.f);
         }
-        const int row = i < n ? rows.next(g) : 0;
-        if (m.first >> i & 1u) {
-          if (a.h0)
-            u[i] = fma4(al[i],
-                        m.first & ((1u << i) - 1u) ? load4(a.h0 + state_row(a, m.first, i, m.first_seq, row) + c) : entry,
-                        u[i]);
-          s = Span{all4(1.f), u[i]};
-        } else {
+        if (m.first >> i & 1u)
+          s = Span{all4(0.f), u[i]};
+        else
           s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), fma4(al[i], s.h, u[i])};
-        }
       }
-      odd = m.first != 0u || !all_within(s.A, 1.f);
-      if (m.first) s.A.a.x = -0.f;
+      odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
     }
+    if (m.first) s.A.a.x = -0.f;
     F4 h;
     const bool going = walk.exchange(s, odd, packed, round, h, grown, [&] {
       // The tokens are in registers: their slots are free for the next round's.
@@ -127,27 +131,36 @@ __global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3)
     if (!going) break;
     Rows rows(g, p0, 1);
     int apart;
-    if (plain && m.last == 0u && rows.even(g, kRun, apart) && (!packed || m.inside == (1u << kRun) - 1u)) {
-      T* po = out + (int64_t)rows.next(g) * a.C;
-      const int64_t d = (int64_t)apart * a.C;
+    if (!rows.even(g, kRun, apart)) {  // grids alone
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        h = fma4(al[i], h, u[i]);
+        if (i < n) store4(out + (int64_t)rows.next(g) * a.C, h);
+      }
+      continue;
+    }
+    const uint32_t write = packed ? m.inside : (1u << n) - 1u;
+    T* po = out + (int64_t)rows.next(g) * a.C;
+    const int64_t d = (int64_t)apart * a.C;
+    if (write == (1u << kRun) - 1u && (m.first | m.last) == 0u) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         h = fma4(al[i], h, u[i]);
         store4(po, h);
         po += d;
       }
-    } else {
+      continue;
+    }
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        if (i >= n) break;
-        const int row = rows.next(g);
-        h = m.first >> i & 1u ? u[i] : fma4(al[i], h, u[i]);
-        if (!packed || (m.inside >> i & 1u))
-          store4(out + (int64_t)row * a.C, h);
-        else if (a.fill)
-          store4(out + (int64_t)row * a.C, all4(0.f));
-        if (a.h_last && (m.last >> i & 1u)) store4(a.h_last + state_row(a, m.last, i, m.last_seq, row) + c, h);
-      }
+    for (int i = 0; i < kRun; ++i) {
+      h = m.first >> i & 1u ? u[i] : fma4(al[i], h, u[i]);
+      if (write >> i & 1u)
+        store4(po, h);
+      else if (a.fill && i < n)
+        store4(po, all4(0.f));
+      if (a.h_last && (m.last >> i & 1u))
+        store4(a.h_last + state_row(a, m.last, i, m.last_seq, a.dir ? g.T - 1 - (p0 + i) : p0 + i) + c, h);
+      po += d;
     }
   }
   cp_async_wait_all();

@@ -45,8 +45,16 @@ __device__ __forceinline__ bool forgets(const Span& s) { return (int)__float_as_
 
 __device__ __forceinline__ F4 enter(const Span& s, F4 in) { return fma4(s.A, in, s.h); }
 __device__ __forceinline__ F4 enter_marked(const Span& s, F4 in) { return forgets(s) ? s.h : enter(s, in); }
+// The mark of two spans: that of either.
+__device__ __forceinline__ float marked(float A, const Span& first, const Span& then) {
+  return __uint_as_float((__float_as_uint(A) & ~kForget) |
+                         ((__float_as_uint(first.A.a.x) | __float_as_uint(then.A.a.x)) & kForget));
+}
+// Two spans as one.  A marked span has A = 0 as well, so this is right for finite values.
 __device__ __forceinline__ Span join(const Span& first, const Span& then) {
-  return Span{mul4(first.A, then.A), enter(then, first.h)};
+  Span r{mul4(first.A, then.A), enter(then, first.h)};
+  r.A.a.x = marked(r.A.a.x, first, then);
+  return r;
 }
 
 __device__ __forceinline__ bool any_over(F4 v, float most) {  // (a NaN compares false)
@@ -55,6 +63,10 @@ __device__ __forceinline__ bool any_over(F4 v, float most) {  // (a NaN compares
 __device__ __forceinline__ bool all_within(F4 v, float most) {  // (a NaN compares false)
   return v.a.x <= most && v.a.y <= most && v.b.x <= most && v.b.y <= most;
 }
+__device__ __forceinline__ bool finite4(F4 v) {
+  const float2 s = __fmul2_rn(__fadd2_rn(v.a, v.b), both(0.f));
+  return s.x + s.y == 0.f;  // (sums that overflow count as not finite)
+}
 // Growth is held at the largest fp32 number (and reported), so that a zero that enters
 // later gives zero instead of NaN.
 __device__ __forceinline__ F4 capped(F4 v, bool& grown) {
@@ -62,11 +74,10 @@ __device__ __forceinline__ F4 capped(F4 v, bool& grown) {
   auto c = [](float x) { return x > FLT_MAX ? FLT_MAX : x; };
   return F4{make_float2(c(v.a.x), c(v.a.y)), make_float2(c(v.b.x), c(v.b.y))};
 }
-// join() where a span may be marked or may grow: a mark in either stays.
+// join() where a value may not be finite (it ends at a mark) or a span may grow.
 __device__ __forceinline__ Span join_marked(const Span& first, const Span& then, bool& grown) {
   Span r{capped(mul4(first.A, then.A), grown), enter_marked(then, first.h)};
-  r.A.a.x = __uint_as_float((__float_as_uint(r.A.a.x) & ~kForget) |
-                            ((__float_as_uint(first.A.a.x) | __float_as_uint(then.A.a.x)) & kForget));
+  r.A.a.x = marked(r.A.a.x, first, then);
   return r;
 }
 
@@ -135,9 +146,9 @@ struct Walk {
   }
 
   // The value that enters this thread's span s.  Returns false, in all threads of the block
-  // alike, when the wait for the other blocks ran out.  odd: s is marked, or its A may exceed
-  // 1 (without either no product of spans can overflow or must forget).  marks: spans of the
-  // slab may be marked.  meanwhile() runs while the totals travel: the next round's copies
+  // alike, when the wait for the other blocks ran out.  odd: s is not finite or its A may
+  // exceed 1 (otherwise no product of spans overflows, and A = 0 forgets).  marks: spans of
+  // the slab may be marked.  meanwhile() runs while the totals travel: the next round's copies
   // and searches.
   //
   // Reuse of the buffers: a block sends its total of round k + 2 only after it has received

@@ -312,6 +312,11 @@ def _dense(t, name: str, dtype: torch.dtype, dev: torch.device, index: int, shap
         raise ValueError(f"{name} must be {list(shape)} (got {list(t.shape)})")
 
 
+def _new(t):
+    """A dense tensor of t's shape and type."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _row_stride(t: torch.Tensor, name: str, lead: int, inner: int) -> int:
     """Elements between token rows of t, whose first `lead` dimensions are tokens (batches
     behind one another without a gap) and whose other dimensions are dense, `inner` elements."""
@@ -402,7 +407,7 @@ def _glr_fwd(fn, x, gate, where, direction, gate_norm, complement, h0, out, h_la
         _dense(h0, "h0", torch.float32, dev, index, states)
     fill = out is None
     if fill:
-        out = x.new_empty(shape)
+        out = _new(x)
     else:
         _dense(out, "out", x.dtype, dev, index, shape)
     if h_last is None:
@@ -449,11 +454,11 @@ def _glr_bwd(fn, x, gate, h, dout, where, direction, gate_norm, complement, h0, 
         raise ValueError("give both dx and dgate, or neither")
     fill = dx is None
     if fill:
-        dx = x.new_empty(shape)
+        dx = _new(x)
     else:
         _dense(dx, "dx", x.dtype, dev, index, shape)
     if dgate is None:
-        dgate = gate.new_empty(shape)
+        dgate = _new(gate)
     else:
         _dense(dgate, "dgate", gate.dtype, dev, index, shape)
     if dh0 is None:
@@ -498,7 +503,7 @@ def glr_step(x, gate, state, slots=None, gate_norm: float | None = None, complem
         _dense(slots, "slots", torch.int32, dev, index, (N,))
     fill = out is None
     if fill:
-        out = x.new_empty(shape)
+        out = _new(x)
     else:
         _dense(out, "out", x.dtype, dev, index, shape)
     if state_out is None:
@@ -556,27 +561,37 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
     return inv.to(torch.float32).to(device or "cpu"), scale
 
 
-def _heads(t, name: str, dtype, dev, index: int, lead, D: int):
-    """Checks a tensor of heads [*lead, H, D]; (H, its row stride)."""
-    _on(t, name, dtype, dev, index)
+def _heads(t, name: str, dtype, dev, index: int, like):
+    """Checks a tensor of heads [*rows, H, D] whose rows and D are those of the shape `like`;
+    (H, its row stride)."""
+    if not (isinstance(t, _Tensor) and t.dtype is dtype and t.get_device() == index):
+        _refuse(t, name, dtype, dev, False)
     shape = t.shape
-    if len(shape) != len(lead) + 2 or shape[-1] != D or shape[:-2] != lead:
+    n = len(like)
+    if len(shape) != n or shape[0] != like[0] or shape[-1] != like[-1] or (n == 4 and shape[1] != like[1]):
         raise ValueError(f"{name}: expected [rows,H,D] or [B,T,H,D] with the rows and D of the queries")
-    return shape[-2], _row_stride(t, name, len(lead), shape[-2] * D)
+    H, D = shape[-2], shape[-1]
+    if t.is_contiguous():
+        return H, H * D
+    if n == 3:
+        stride = t.stride()
+        if stride[2] == 1 and stride[1] == D and shape[0] != 1:
+            return H, stride[0]
+    return H, _row_stride(t, name, n - 2, H * D)
 
 
-def _head_out(t, name: str, like, dtype, dev, index: int, lead, H: int, D: int):
+def _head_out(t, name: str, like, dtype, dev, index: int, H: int):
     """A caller's output of `like`'s shape, or a new dense one; with its row stride."""
     if t is None:
-        return like.new_empty(like.shape), H * D
-    h, stride = _heads(t, name, dtype, dev, index, lead, D)
+        return _new(like), H * like.shape[-1]
+    h, stride = _heads(t, name, dtype, dev, index, like.shape)
     if h != H:
         raise ValueError(f"{name} must be {list(like.shape)} (got {list(t.shape)})")
     return t, stride
 
 
 def _queries(q):
-    """(device, its index, dtype, dtype code, leading dimensions, rows, D) of the queries."""
+    """(device, its index, dtype, dtype code, shape, rows) of the queries."""
     if not isinstance(q, _Tensor):
         raise TypeError("q must be a torch.Tensor")
     dt, shape, dev, index = _grid_dtype(q), q.shape, q.device, q.get_device()
@@ -584,41 +599,48 @@ def _queries(q):
         raise ValueError("q: expected [rows,H,D] or [B,T,H,D]")
     if index < 0:
         _refuse(q, "q", q.dtype, dev)
-    lead = shape[:-2]
-    return dev, index, q.dtype, dt, lead, lead.numel(), shape[-1]
+    return dev, index, q.dtype, dt, shape, shape[0] if len(shape) == 3 else shape[0] * shape[1]
 
 
-def _angle_args(positions, inv_freq, dev, index, lead, rows):
+def _angle_args(positions, inv_freq, dev, index, shape, rows):
     """C arguments of the positions and the table, and rot."""
     at, wide = None, 0
     if positions is not None:
         if not isinstance(positions, _Tensor) or positions.dtype not in (torch.int32, torch.int64):
             raise TypeError("positions must be an int32 or int64 tensor")
         wide = int(positions.dtype is torch.int64)
-        _dense(positions, "positions", positions.dtype, dev, index, lead)
+        if positions.get_device() != index or not positions.is_contiguous():
+            _refuse(positions, "positions", positions.dtype, dev)
+        if positions.shape != shape[:-2]:
+            raise ValueError("positions must be one for each row of q")
         at = positions.data_ptr()
     rot, table = 0, None
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel() if isinstance(inv_freq, _Tensor) else 0
-        _dense(inv_freq, "inv_freq", torch.float32, dev, index, (rot // 2,))
-        table = inv_freq.data_ptr()
-    return (at, wide, lead[-1], table, rows), rot
+        if not (isinstance(inv_freq, _Tensor) and inv_freq.dtype is torch.float32 and inv_freq.get_device() == index
+                and inv_freq.is_contiguous()):
+            _refuse(inv_freq, "inv_freq", torch.float32, dev)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be [rot/2]")
+        rot, table = 2 * inv_freq.numel(), inv_freq.data_ptr()
+    return (at, wide, shape[-3], table, rows), rot
 
 
 def _rope_call(fn, q, k, weights, positions, inv_freq, middle, q_out, k_out, stream):
-    dev, index, dtype, dt, lead, rows, D = _queries(q)
-    angles, rot = _angle_args(positions, inv_freq, dev, index, lead, rows)
+    dev, index, dtype, dt, shape, rows = _queries(q)
+    D = shape[-1]
+    angles, rot = _angle_args(positions, inv_freq, dev, index, shape, rows)
     w = _weights(k, *weights, dev, index, D) if weights else ()
-    H, qs = _heads(q, "q", dtype, dev, index, lead, D)
-    q_out, qos = _head_out(q_out, "q_out", q, dtype, dev, index, lead, H, D)
-    Hk, ks, kos = 0, D, D
+    H, qs = _heads(q, "q", dtype, dev, index, shape)
+    q_out, qos = _head_out(q_out, "q_out", q, dtype, dev, index, H)
+    Hk, ks, kos, pk, pko = 0, D, D, None, None
     if k is not None:
-        Hk, ks = _heads(k, "k", dtype, dev, index, lead, D)
-        k_out, kos = _head_out(k_out, "k_out", k, dtype, dev, index, lead, Hk, D)
+        Hk, ks = _heads(k, "k", dtype, dev, index, shape)
+        k_out, kos = _head_out(k_out, "k_out", k, dtype, dev, index, Hk)
+        pk, pko = k.data_ptr(), k_out.data_ptr()
     elif k_out is not None:
         raise ValueError("k_out without k")
-    _call(fn, dev, index, stream, q.data_ptr(), _ptr(k), *w, *angles, H, Hk, D, rot, qs, ks, *middle, dt,
-          q_out.data_ptr(), qos, _ptr(k_out), kos)
+    _call(fn, dev, index, stream, q.data_ptr(), pk, *w, *angles, H, Hk, D, rot, qs, ks, *middle, dt, q_out.data_ptr(), qos,
+          pko, kos)
     return q_out, k_out
 
 
@@ -657,23 +679,24 @@ def qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, positions, inv_fr
     """The gradients of qk_norm_rope (see include/dig_gla.h, qk_norm_rope_bwd) from its inputs and
     those of its outputs.  dq and dk may be dq_out and dk_out.  Returns (dq, dk, dq_weight fp32,
     dk_weight fp32)."""
-    dev, index, dtype, dt, lead, rows, D = _queries(q)
-    angles, rot = _angle_args(positions, inv_freq, dev, index, lead, rows)
+    dev, index, dtype, dt, shape, rows = _queries(q)
+    D = shape[-1]
+    angles, rot = _angle_args(positions, inv_freq, dev, index, shape, rows)
     w = _weights(k, q_weight, k_weight, dev, index, D)
-    H, qs = _heads(q, "q", dtype, dev, index, lead, D)
-    h, dqs = _heads(dq_out, "dq_out", dtype, dev, index, lead, D)
+    H, qs = _heads(q, "q", dtype, dev, index, shape)
+    h, dqs = _heads(dq_out, "dq_out", dtype, dev, index, shape)
     if h != H:
         raise ValueError("dq_out must have q's shape")
-    dq, dqo = _head_out(dq, "dq", q, dtype, dev, index, lead, H, D)
-    dwq = q_weight.new_empty((D,))
+    dq, dqo = _head_out(dq, "dq", q, dtype, dev, index, H)
+    dwq = torch.empty_like(q_weight)
     Hk, ks, dks, dko, dwk = 0, D, D, D, None
     if k is not None:
-        Hk, ks = _heads(k, "k", dtype, dev, index, lead, D)
-        h, dks = _heads(dk_out, "dk_out", dtype, dev, index, lead, D)
+        Hk, ks = _heads(k, "k", dtype, dev, index, shape)
+        h, dks = _heads(dk_out, "dk_out", dtype, dev, index, shape)
         if h != Hk:
             raise ValueError("dk_out must have k's shape")
-        dk, dko = _head_out(dk, "dk", k, dtype, dev, index, lead, Hk, D)
-        dwk = q_weight.new_empty((D,))
+        dk, dko = _head_out(dk, "dk", k, dtype, dev, index, Hk)
+        dwk = torch.empty_like(k_weight)
     elif dk_out is not None or dk is not None:
         raise ValueError("dk_out or dk without k")
     _call(_lib.qk_norm_rope_bwd, dev, index, stream, dq_out.data_ptr(), _ptr(dk_out), q.data_ptr(), _ptr(k), *w, *angles, H,

@@ -1,5 +1,14 @@
 // glr_step.cu -- one token of the gated linear recurrence for every running sequence
 // (include/dig_gla.h, glr_step).
+//
+// Bound: memory, and for few rows the latency of one load after another (slot, then state).
+// A block takes one row, or with few rows a part of its channels; a thread takes four
+// channels at a time.  The rows of one slot are its successive tokens: the block of the first
+// of them applies them all in row order and the others leave, so no two blocks touch a
+// state, whatever the slots hold.  Finding that out is one pass over the slots by the block's
+// threads while the row's own loads are under way.
+#include <algorithm>
+
 #include "glr.cuh"
 
 namespace dig {
@@ -8,47 +17,73 @@ namespace {
 
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ float load_f32(const float* p) { return *p; }
-__device__ __forceinline__ float load_f32(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
-// One thread per (row, channel).  Rows that name the same state belong together: the
-// first of them applies all, in row order, the others do nothing.
-template <typename T, int kKind>
-__global__ void __launch_bounds__(kThreads) glr_step_k(GlrStepArgs a, int cblocks) {
+template <typename T, int kKind, bool kComp>
+__global__ void __launch_bounds__(kThreads) glr_step_k(GlrStepArgs a, int parts) {
   using G = GateT<T, kKind>;
-  const T* x = static_cast<const T*>(a.x);
-  const G* gate = static_cast<const G*>(a.gate);
-  T* out = static_cast<T*>(a.out);
-  const int i = blockIdx.x / cblocks;
-  const int c = (blockIdx.x - i * cblocks) * kThreads + threadIdx.x;
-  if (c >= a.C) return;
+  const T* const x = static_cast<const T*>(a.x);
+  const G* const gate = static_cast<const G*>(a.gate);
+  T* const out = static_cast<T*>(a.out);
+  const int i = blockIdx.x / parts, part = blockIdx.x - i * parts;
   const int slot = a.slots ? a.slots[i] : i;
+  const int c0 = (part * kThreads + threadIdx.x) * 4, step = parts * kThreads * 4;
   if (slot < 0 || slot >= a.nslots) {
-    if (slot >= a.nslots) report_status(GLA_ERR_INVALID_ARG);
-    if (a.fill) store_f32(out + (int64_t)i * a.C + c, 0.f);
+    if (slot >= a.nslots && threadIdx.x == 0) report_status(GLA_ERR_INVALID_ARG);
+    if (a.fill)
+      for (int c = c0; c < a.C; c += step) store4(out + (int64_t)i * a.C + c, all4(0.f));
     return;
   }
   const float inv_norm = 1.f / a.gate_norm;
-  if (a.slots)
-    for (int j = 0; j < i; ++j)
-      if (a.slots[j] == slot) return;
-  float h = a.state[(int64_t)slot * a.C + c];
-  for (int j = i; j < a.N; ++j) {
-    if (j != i && (!a.slots || a.slots[j] != slot)) continue;
-    const Gates k = make_gates<kKind>(both(load_f32(gate + j * a.gate_stride + c)), inv_norm);
-    const float u = load_f32(x + j * a.x_stride + c);
-    h = fmaf(k.alpha.x, h, a.complement ? k.rest.x * u : u);
-    store_f32(out + (int64_t)j * a.C + c, h);
+  const float* const from = a.state + (int64_t)slot * a.C;
+  float* const to = a.state_out + (int64_t)slot * a.C;
+  // The first four channels' loads go out before the search for other rows of the slot.
+  F4 h = all4(0.f), u = all4(0.f), g = all4(0.f);
+  if (c0 < a.C) {
+    h = load4(from + c0);
+    u = load4(x + i * a.x_stride + c0);
+    g = load4(gate + i * a.gate_stride + c0);
   }
-  a.state_out[(int64_t)slot * a.C + c] = h;
+  bool before = false, behind = false;
+  if (a.slots) {
+    for (int j = threadIdx.x; j < a.N; j += kThreads) {
+      const bool same = a.slots[j] == slot;
+      before |= same && j < i;
+      behind |= same && j > i;
+    }
+    if (__syncthreads_or(before)) return;
+    behind = __syncthreads_or(behind);
+  }
+  for (int c = c0; c < a.C; c += step) {
+    if (c != c0) {
+      h = load4(from + c);
+      u = load4(x + i * a.x_stride + c);
+      g = load4(gate + i * a.gate_stride + c);
+    }
+    for (int j = i;;) {
+      const Gates4 k = make_gates4<kKind>(g, inv_norm);
+      h = fma4(k.alpha, h, kComp ? mul4(k.rest, u) : u);
+      store4(out + (int64_t)j * a.C + c, h);
+      if (!behind) break;
+      do ++j;
+      while (j < a.N && a.slots[j] != slot);
+      if (j >= a.N) break;
+      u = load4(x + j * a.x_stride + c);
+      g = load4(gate + j * a.gate_stride + c);
+    }
+    store4(to + c, h);
+  }
 }
 
 template <typename T, int kKind>
 cudaError_t launch(const GlrStepArgs& a, cudaStream_t st) {
-  const int cblocks = (a.C + kThreads - 1) / kThreads;
-  glr_step_k<T, kKind><<<(unsigned)cblocks * a.N, kThreads, 0, st>>>(a, cblocks);
+  // A row is shared between blocks while there are fewer than 8 blocks an SM; a block that
+  // takes a whole row searches the slots once for all its channels.
+  const int chunks = (a.C + 4 * kThreads - 1) / (4 * kThreads);
+  const int parts = std::max(1, std::min(chunks, 148 * 8 / a.N));
+  const unsigned grid = (unsigned)parts * a.N;
+  if (a.complement)
+    glr_step_k<T, kKind, true><<<grid, kThreads, 0, st>>>(a, parts);
+  else
+    glr_step_k<T, kKind, false><<<grid, kThreads, 0, st>>>(a, parts);
   return cudaGetLastError();
 }
 

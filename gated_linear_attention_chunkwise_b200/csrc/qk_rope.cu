@@ -328,18 +328,18 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, 
           }
         }
         float sd[2 * kHeads];
+        Pairs turned[kHeads];
 #pragma unroll
         for (int k = 0; k < kHeads; ++k) {
           const Pairs x = as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k]));
           Pairs g = as_pairs<kInter>(Four<T>::get(ga[k]), Four<T>::get(gb[k]));
           if (at.turned) g = mix(g, back);
+          turned[k] = g;
           const Pairs wx = times(x, weight);
           sd[2 * k] = sum4(fma4(x.y, x.y, mul4(x.x, x.x)));
           sd[2 * k + 1] = sum4(fma4(wx.y, g.y, mul4(wx.x, g.x)));
           xa[k] = again(xa[k]);
           xb[k] = again(xb[k]);
-          ga[k] = again(ga[k]);
-          gb[k] = again(gb[k]);
         }
         group_sum(sd, at.g);
 #pragma unroll
@@ -347,8 +347,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, 
           if (head + k * at.groups >= end) continue;
           const float r = rsqrtf(sd[2 * k] * inv_d + a.eps);
           const float m = sd[2 * k + 1] * r * inv_d;
-          Pairs g = as_pairs<kInter>(Four<T>::get(ga[k]), Four<T>::get(gb[k]));
-          if (at.turned) g = mix(g, back);
+          const Pairs g = turned[k];
           const Pairs n = scaled(as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k])), r);
           dw[which] = Pairs{fma4(g.x, n.x, dw[which].x), fma4(g.y, n.y, dw[which].y)};
           // r (w g - m n)

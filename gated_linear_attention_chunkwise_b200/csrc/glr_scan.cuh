@@ -426,10 +426,20 @@ inline cudaError_t enqueue(Kernel k, Known& known, const GlrArgs& a, const ScanG
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
     known[dev & 63][0].store(1, std::memory_order_relaxed);
   }
-  // The widest cluster that has tokens for all its blocks and whose copies, one a slab, all
-  // run at once (a second wave of a few clusters would double the time).
-  int cluster = (int)std::min<int64_t>(kMaxCluster, ((int64_t)g.T + per_block - 1) / per_block);
-  while (cluster > 1 && (int64_t)a.B * slabs > resident_clusters(k, cluster, smem, known[dev & 63])) --cluster;
+  // The cluster size that ends first, counted in rounds: clusters that run at once, wave
+  // after wave, each with two rounds' worth of start and end.
+  const int64_t total = (int64_t)a.B * slabs;
+  int cluster = 1;
+  int64_t least = INT64_MAX;
+  for (int size = 1; size <= kMaxCluster && (size == 1 || (int64_t)(size - 1) * per_block < g.T); ++size) {
+    const int64_t at_once = resident_clusters(k, size, smem, known[dev & 63]);
+    const int64_t per_round = (int64_t)size * per_block;
+    const int64_t cost = (total + at_once - 1) / at_once * ((g.T + per_round - 1) / per_round + 2);
+    if (cost < least) {
+      least = cost;
+      cluster = size;
+    }
+  }
   const int64_t per_round = (int64_t)cluster * per_block;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;

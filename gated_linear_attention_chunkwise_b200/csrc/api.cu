@@ -155,13 +155,18 @@ cudaMemPool_t workspace_pool(int dev) {
     props.location.type = cudaMemLocationTypeDevice;
     props.location.id = dev;
     cudaMemPool_t p = nullptr;
-    if (cudaMemPoolCreate(&p, &props) != cudaSuccess) {
+    // The first call may be one that is captured into a graph; creating a pool touches no
+    // stream, but a capture refuses it unless this thread's mode is relaxed meanwhile.
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    cudaThreadExchangeStreamCaptureMode(&mode);
+    if (cudaMemPoolCreate(&p, &props) == cudaSuccess) {
+      uint64_t keep = UINT64_MAX;
+      cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+      g_pool[dev] = p;
+    } else {
       cudaGetLastError();
-      return nullptr;
     }
-    uint64_t keep = UINT64_MAX;
-    cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
-    g_pool[dev] = p;
+    cudaThreadExchangeStreamCaptureMode(&mode);
   }
   return g_pool[dev];
 }

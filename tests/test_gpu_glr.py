@@ -403,3 +403,102 @@ def test_prompts_then_tokens_equal_the_whole(dig):
         got, _ = dig.glr_step(x[here].contiguous(), gate[here].contiguous(), pool, slots, gate_norm=16.0, complement=True)
         h = here.cpu().numpy()
         ref.check(np64(got), w[0][h], 2 * w[2][h], f"token {t}")
+
+
+@pytest.mark.parametrize("d", [0, 1])
+def test_padding_may_hold_anything(dig, d):
+    """NaN and infinities in rows of no sequence, before the first and behind the last, change nothing."""
+    rows, C, cu = 900, 72, [70, 71, 400, 401, 830]
+    dcu = torch.tensor(cu, dtype=torch.int32).cuda()
+    for gate_norm, comp in ((None, False), (16.0, True)):
+        x, gate = inputs(30, (rows,), C, torch.float32, gate_norm)
+        h0, dout, dlast = normal(31, (4, C)), normal(32, (rows, C)), normal(33, (4, C))
+        out, last = dig.glr_fwd_packed(x, gate, dcu, d, gate_norm, comp, h0=h0)
+        grads = dig.glr_bwd_packed(x, gate, out, dout, dcu, d, gate_norm, comp, h0=h0, dh_last=dlast)
+        junk = [t.clone() for t in (x, gate, out, dout)]
+        for t, v in zip(junk, (float("nan"), float("inf"), float("nan"), -float("inf"))):
+            t[:70], t[830:] = v, v
+        junk[1][40:60] = float("nan")
+        again = dig.glr_fwd_packed(junk[0], junk[1], dcu, d, gate_norm, comp, h0=h0)
+        more = dig.glr_bwd_packed(*junk, dcu, d, gate_norm, comp, h0=h0, dh_last=dlast)
+        for p, q in zip((out, last, *grads), (*again, *more)):
+            assert torch.allclose(p, q, rtol=1e-5, atol=1e-6) and not bool(torch.isnan(q).any())
+    dig.device_status()   # infinite log gates in the padding count as growth
+
+
+@pytest.mark.parametrize("reverse", [0, 1])
+def test_a_nan_ends_with_its_sequence(dig, reverse):
+    """Whatever the cut: a NaN at any place of a sequence leaves its neighbours as they were."""
+    rows, C = 600, 64
+    cu = [0, 3, 130, 131, 260, 264, 600]
+    dcu = torch.tensor(cu, dtype=torch.int32).cuda()
+    x, gate = inputs(34, (rows,), C, torch.float32, 1.0)
+    dout = normal(35, (rows, C))
+    out, last = dig.glr_fwd_packed(x, gate, dcu, reverse, 1.0)
+    dx, dg, dh0 = dig.glr_bwd_packed(x, gate, out, dout, dcu, reverse, 1.0)
+    for n, at in ((0, 1), (1, 3), (1, 129), (2, 130), (3, 200), (4, 263)):
+        bad = x.clone()
+        bad[at] = float("nan")
+        o, l = dig.glr_fwd_packed(bad, gate, dcu, reverse, 1.0)
+        keep = torch.ones(rows, dtype=torch.bool)
+        keep[cu[n]:cu[n + 1]] = False
+        keep = keep.cuda()
+        assert torch.allclose(o[keep], out[keep], rtol=1e-5, atol=1e-6), (n, at)
+        assert bool(torch.isnan(o[at]).all()) and bool(torch.isnan(l[n]).all())
+        others = [k for k in range(6) if k != n]
+        assert torch.allclose(l[others], last[others], rtol=1e-5, atol=1e-6)
+        bad = dout.clone()
+        bad[at] = float("nan")
+        px, pg, p0 = dig.glr_bwd_packed(x, gate, out, bad, dcu, reverse, 1.0)
+        assert torch.allclose(px[keep], dx[keep], rtol=1e-5, atol=1e-6) and torch.allclose(pg[keep], dg[keep], rtol=1e-5, atol=1e-6)
+        assert torch.allclose(p0[others], dh0[others], rtol=1e-5, atol=1e-6) and bool(torch.isnan(p0[n]).all())
+    assert dig.device_status() == 0
+
+
+def test_two_calls_at_once(dig):
+    """Long and short calls on two streams at the same time, each with its own results."""
+    xs = [inputs(40 + i, (1, T), 512, torch.bfloat16, 16.0) for i, T in enumerate((20000, 700))]
+    want = [dig.glr_fwd(x, g, 1, x.shape[1], 0, gate_norm=16.0) for x, g in xs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, (x, g) in enumerate(xs):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(dig.glr_fwd(x, g, 1, x.shape[1], 0, gate_norm=16.0))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(l, want[i][1])
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """Nothing a first call sets up needs an eager call before."""
+    import subprocess
+    import sys
+    code = """
+import torch, gated_linear_attention_chunkwise_b200 as dig
+x, g = torch.randn(1, 3000, 256, device="cuda"), -torch.rand(1, 3000, 256, device="cuda")
+q, w, inv = torch.randn(40, 4, 64, device="cuda"), torch.ones(64, device="cuda"), dig.rope_frequencies(64, device="cuda")[0]
+s = torch.zeros(3, 256, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    o, l = dig.glr_fwd(x, g, 1, 3000, 0)
+    d = dig.glr_bwd(x, g, o, x, 1, 3000, 0)
+    n = dig.qk_norm_rope(q, None, w, None, None, inv)
+    b = dig.qk_norm_rope_bwd(n[0], None, q, None, w, None, None, inv)
+    t = dig.glr_step(x[0, :3], g[0, :3], s, state_out=torch.empty_like(s))
+graph.replay(); graph.replay()
+got = [v.clone() for v in (o, l, *d, n[0], b[0], b[2], *t)]
+o, l = dig.glr_fwd(x, g, 1, 3000, 0)
+n = dig.qk_norm_rope(q, None, w, None, None, inv)
+b = dig.qk_norm_rope_bwd(n[0], None, q, None, w, None, None, inv)
+want = (o, l, *dig.glr_bwd(x, g, o, x, 1, 3000, 0), n[0], b[0], b[2], *dig.glr_step(x[0, :3], g[0, :3], s, state_out=torch.empty_like(s)))
+assert all(torch.equal(p, q) for p, q in zip(got, want))
+print("same")
+"""
+    import os
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=root)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

@@ -314,7 +314,7 @@ def _dense(t, name: str, dtype: torch.dtype, dev: torch.device, index: int, shap
 
 def _new(t):
     """A dense tensor of t's shape and type."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def _row_stride(t: torch.Tensor, name: str, lead: int, inner: int) -> int:
@@ -378,7 +378,7 @@ def _gated(x, gate, gate_norm, dims: int):
     _on(gate, "gate", gtype, dev, index)
     if len(shape) != dims or gate.shape != shape:
         raise ValueError(f"expected x and gate of the same {dims}-dimensional shape")
-    if max(shape) >= 1 << 31:
+    if x.numel() >= 1 << 31 and max(shape) >= 1 << 31:
         raise ValueError("x: a dimension of 2^31 or more")
     C = shape[-1]
     return dev, index, shape, dt, norm, _row_stride(x, "x", dims - 1, C), _row_stride(gate, "gate", dims - 1, C)
@@ -411,7 +411,7 @@ def _glr_fwd(fn, x, gate, where, direction, gate_norm, complement, h0, out, h_la
     else:
         _dense(out, "out", x.dtype, dev, index, shape)
     if h_last is None:
-        h_last = torch.empty(states, dtype=torch.float32, device=dev)
+        h_last = torch.empty(states, dtype=torch.float32, device=dev) if h0 is None else torch.empty_like(h0)
     else:
         _dense(h_last, "h_last", torch.float32, dev, index, states)
     _call(fn, dev, index, stream, x.data_ptr(), gate.data_ptr(), *((where[0].data_ptr(),) if packed else ()), _ptr(h0),
@@ -462,7 +462,7 @@ def _glr_bwd(fn, x, gate, h, dout, where, direction, gate_norm, complement, h0, 
     else:
         _dense(dgate, "dgate", gate.dtype, dev, index, shape)
     if dh0 is None:
-        dh0 = torch.empty(states, dtype=torch.float32, device=dev)
+        dh0 = torch.empty(states, dtype=torch.float32, device=dev) if h0 is None else torch.empty_like(h0)
     else:
         _dense(dh0, "dh0", torch.float32, dev, index, states)
     _call(fn, dev, index, stream, x.data_ptr(), gate.data_ptr(), h.data_ptr(), dout.data_ptr(),

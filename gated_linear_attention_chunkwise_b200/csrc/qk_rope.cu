@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
 
 // ---- gradients ------------------------------------------------------------------------------
 // Warps walk the items with a stride and keep the weight gradients of their lanes' channels;
-// a block adds its groups and warps in a fixed order and writes one row for q and one for k.
+// a block adds its heads and warps in a fixed order and writes a column for q and one for k.
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
   using Raw = typename Four<T>::Raw;
@@ -391,16 +391,17 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, 
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) s += sums[i][which][ch];
-    part_sums[((int64_t)which * gridDim.x + blockIdx.x) * a.D + ch] = s;
+    part_sums[((int64_t)which * a.D + ch) * gridDim.x + blockIdx.x] = s;
   }
 }
 
-// The blocks' rows: a warp a channel, its lanes a stride of rows, then a tree over the lanes.
+// The blocks' sums, [q, k][channel][block]: a warp a channel, then a tree over its lanes.
 __global__ void __launch_bounds__(256) qk_weight_grad_k(QkRopeArgs a, const float* part, int blocks) {
   const int which = blockIdx.y, ch = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const float* p = part + (int64_t)which * blocks * a.D + ch;
+  const float* p = part + ((int64_t)which * a.D + ch) * blocks;
   float s = 0.f;
-  for (int b = lane; b < blocks; b += 32) s += p[(int64_t)b * a.D];
+#pragma unroll 8
+  for (int b = lane; b < blocks; b += 32) s += p[b];
 #pragma unroll
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (lane == 0) (which ? a.k.dweight : a.q.dweight)[ch] = s;

@@ -216,14 +216,10 @@ template <typename T, int kKind, bool kComp>
 struct Backward {
   static cudaError_t run(const GlrArgs& a, cudaStream_t st) {
     constexpr int kRun = 4;
-    const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
     const size_t smem = (size_t)kRun * kThreads *
                         ((kComp ? 3 : 2) * sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
-    const int64_t wide = (int64_t)a.B * ((a.C + 31) / 32);
     static Known known8, known4;
-    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 8 * kRun)
-      return enqueue(glr_bwd_k<T, kKind, kComp, 8, kRun>, known8, a, g, 8, kRun, smem, st);
-    return enqueue(glr_bwd_k<T, kKind, kComp, 4, kRun>, known4, a, g, 4, kRun, smem, st);
+    return enqueue(glr_bwd_k<T, kKind, kComp, 8, kRun>, known8, glr_bwd_k<T, kKind, kComp, 4, kRun>, known4, a, kRun, smem, st);
   }
 };
 

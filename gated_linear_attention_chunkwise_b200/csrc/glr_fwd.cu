@@ -6,8 +6,14 @@ namespace dig {
 namespace glr {
 namespace {
 
+// Blocks an SM that the registers allow: with log_alpha four (128 registers, the c4 grid 62
+// instead of 68 us with three); the gates of the other forms would spill (packed, logits and
+// complement: 390 us with four, 341 with three).
+constexpr int resident(int kind, bool comp) { return kind == kGateLog && !comp ? 4 : 3; }
+
 template <typename T, int kKind, bool kComp, int kLanes, int kRun>
-__global__ void __launch_bounds__(kThreads, kKind == kGateLog && !kComp ? 4 : 3) glr_fwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
+__global__ void __launch_bounds__(kThreads, resident(kKind, kComp))
+    glr_fwd_k(GlrArgs a, ScanGeom g, int slabs, int rounds) {
   using G = GateT<T, kKind>;
   using RawT = typename Four<T>::Raw;
   using RawG = typename Four<G>::Raw;
@@ -174,13 +180,9 @@ template <typename T, int kKind, bool kComp>
 struct Forward {
   static cudaError_t run(const GlrArgs& a, cudaStream_t st) {
     constexpr int kRun = 8;
-    const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
     const size_t smem = (size_t)kRun * kThreads * (sizeof(typename Four<T>::Raw) + sizeof(typename Four<GateT<T, kKind>>::Raw));
-    const int64_t wide = (int64_t)a.B * ((a.C + 31) / 32);
     static Known known8, known4;
-    if (wide * kMaxCluster >= 148 || g.T <= kThreads / 8 * kRun)
-      return enqueue(glr_fwd_k<T, kKind, kComp, 8, kRun>, known8, a, g, 8, kRun, smem, st);
-    return enqueue(glr_fwd_k<T, kKind, kComp, 4, kRun>, known4, a, g, 4, kRun, smem, st);
+    return enqueue(glr_fwd_k<T, kKind, kComp, 8, kRun>, known8, glr_fwd_k<T, kKind, kComp, 4, kRun>, known4, a, kRun, smem, st);
   }
 };
 

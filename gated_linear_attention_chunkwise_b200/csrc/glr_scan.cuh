@@ -16,8 +16,17 @@
 // slots of shared memory that only it reads while the current round is joined and written.
 //
 // Packed sequences are one long row of tokens; a span that begins a sequence forgets
-// what enters it.  That is marked by the sign bit of A (gates are never negative): the
-// fold then selects instead of multiplying by zero, so a NaN ends with its sequence.
+// what enters it.  It has A = 0, which is all that finite values need, and is marked by the
+// sign bit of A (gates are never negative): where a value is not finite the fold selects
+// instead of multiplying by zero, so a NaN ends with its sequence.
+//
+// What bounds it.  With log_alpha large calls reach 68-80 % of the copy bandwidth (64
+// sequences of 1024 x 2048 bf16: 206 us for 1.07 GB); with logits and the complement form the
+// gates take 16 of 40 instructions an element and it is 36-47 %, half of that issue and half
+// the latency of a round's exchange.  Eight tokens a thread: with 4 the fixed work of a round
+// (330 instructions a thread) doubles an element (one 16384 x 2048 call 68 -> 86 us), with 16
+// the registers leave too few warps (packed, logits: 341 -> 373 us).  128 threads a block:
+// 64 take 385 us there, 256 take 377 us.
 #pragma once
 
 #include <algorithm>
@@ -415,10 +424,21 @@ inline int resident_clusters(Kernel k, int size, size_t smem, std::atomic<int>* 
 // its shared memory is set up.
 using Known = std::atomic<int>[64][kMaxCluster + 1];
 
-inline cudaError_t enqueue(Kernel k, Known& known, const GlrArgs& a, const ScanGeom& g, int lanes, int run, size_t smem,
-                           cudaStream_t st) {
-  const int slabs = (a.C + 4 * lanes - 1) / (4 * lanes);
-  const int per_block = kThreads / lanes * run;
+// How to launch one kernel: clusters of `cluster` blocks over slabs of 4 * lanes channels.
+struct Plan {
+  Kernel kernel;
+  int lanes, slabs, cluster, rounds;
+  float cost;
+};
+
+// The cluster size that ends first.  Waves of clusters that run at once take as many rounds
+// each (and two more to start and end); a round takes the longer the more blocks share an SM.
+// A round of the forward with log_alpha was measured at 2.2 + 0.45 us for each block an SM with
+// 32-channel slabs and 2.3 + 0.55 us with 16-channel slabs: narrow slabs have twice the
+// clusters and half the rounds, and win until the SMs are full (one sequence of 65536 tokens,
+// us wide / narrow: 64 channels 146 / 75, 1024 channels 178 / 142, 2048 channels 242 / 257).
+inline cudaError_t plan(Kernel k, Known& known, const GlrArgs& a, const ScanGeom& g, int lanes, int run, size_t smem,
+                        Plan* best) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -426,33 +446,40 @@ inline cudaError_t enqueue(Kernel k, Known& known, const GlrArgs& a, const ScanG
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
     known[dev & 63][0].store(1, std::memory_order_relaxed);
   }
-  // The cluster size that ends first, counted in rounds: clusters that run at once, wave
-  // after wave, each with two rounds' worth of start and end.
-  const int64_t total = (int64_t)a.B * slabs;
-  int cluster = 1;
-  int64_t least = INT64_MAX;
-  for (int size = 1; size <= kMaxCluster && (size == 1 || (int64_t)(size - 1) * per_block < g.T); ++size) {
+  const int slabs = (a.C + 4 * lanes - 1) / (4 * lanes);
+  const int64_t total = (int64_t)a.B * slabs, per_block = kThreads / lanes * run;
+  for (int size = 1; size <= kMaxCluster && (size == 1 || (size - 1) * per_block < g.T); ++size) {
     const int64_t at_once = resident_clusters(k, size, smem, known[dev & 63]);
-    const int64_t per_round = (int64_t)size * per_block;
-    const int64_t cost = (total + at_once - 1) / at_once * ((g.T + per_round - 1) / per_round + 2);
-    if (cost < least) {
-      least = cost;
-      cluster = size;
-    }
+    const int64_t waves = (total + at_once - 1) / at_once, rounds = (g.T + size * per_block - 1) / (size * per_block);
+    const float sharing = (float)(std::min(total, at_once) * size) / 148.f;
+    const float round = lanes == 8 ? 2.2f + 0.45f * sharing : 2.3f + 0.55f * sharing;
+    const float cost = (float)waves * (float)(rounds + 2) * round;
+    if (cost < best->cost) *best = Plan{k, lanes, slabs, size, (int)rounds, cost};
   }
-  const int64_t per_round = (int64_t)cluster * per_block;
+  return cudaSuccess;
+}
+
+// The cheaper of the kernels with 32- and with 16-channel slabs.
+inline cudaError_t enqueue(Kernel wide, Known& known_wide, Kernel narrow, Known& known_narrow, const GlrArgs& a, int run,
+                           size_t smem, cudaStream_t st) {
+  const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);
+  Plan p{};
+  p.cost = FLT_MAX;
+  cudaError_t e = plan(wide, known_wide, a, g, 8, run, smem, &p);
+  if (e == cudaSuccess && (int64_t)a.B * a.C <= 1 << 20) e = plan(narrow, known_narrow, a, g, 4, run, smem, &p);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = cluster;
+  attr.val.clusterDim.x = p.cluster;
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.gridDim = dim3((unsigned)((int64_t)a.B * slabs * cluster));
+  cfg.gridDim = dim3((unsigned)((int64_t)a.B * p.slabs * p.cluster));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, a, g, slabs, (int)((g.T + per_round - 1) / per_round));
+  return cudaLaunchKernelEx(&cfg, p.kernel, a, g, p.slabs, p.rounds);
 }
 
 // Calls f<T, kind, complement>() for the call's types.

@@ -5,7 +5,7 @@
 // maps the value that enters it to A * in + h, and two spans compose to (A2 A1, A2 h1 + h2),
 // so a long sequence is cut into spans that are folded separately and then joined.
 //
-// Split.  A cluster of up to 8 blocks owns a slab of channels of one sequence (or of the
+// Split.  A cluster of up to 16 blocks owns a slab of channels of one sequence (or of the
 // row of packed sequences) and walks it in rounds.  In a round every thread folds kRun
 // consecutive tokens of four channels in registers; warps join their threads' spans by
 // shuffles, the block its warps' in shared memory, the cluster its blocks' by asynchronous
@@ -39,7 +39,7 @@ namespace glr {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // above 8 a kernel has to be allowed to
 
 // ---- spans of four channels ---------------------------------------------------------------
 struct Span {
@@ -414,7 +414,7 @@ inline int resident_clusters(Kernel k, int size, size_t smem, std::atomic<int>* 
   cfg.numAttrs = 1;
   if (cudaOccupancyMaxActiveClusters(&n, k, &cfg) != cudaSuccess || n < 1) {
     cudaGetLastError();
-    return 1;
+    return size == 1 ? 1 : 0;  // a size that this device does not run
   }
   known[size].store(n, std::memory_order_relaxed);
   return n;
@@ -436,23 +436,28 @@ struct Plan {
 // A round of the forward with log_alpha was measured at 2.2 + 0.45 us for each block an SM with
 // 32-channel slabs and 2.3 + 0.55 us with 16-channel slabs: narrow slabs have twice the
 // clusters and half the rounds, and win until the SMs are full (one sequence of 65536 tokens,
-// us wide / narrow: 64 channels 146 / 75, 1024 channels 178 / 142, 2048 channels 242 / 257).
+// us wide / narrow with clusters of 8: 64 channels 146 / 75, 1024 channels 178 / 142, 2048
+// channels 242 / 257).  Each block above 8 adds 0.12 us to a round, so wider clusters pay
+// while SMs are idle (64 channels 75 -> 45, 256 channels 94 -> 68).
 inline cudaError_t plan(Kernel k, Known& known, const GlrArgs& a, const ScanGeom& g, int lanes, int run, size_t smem,
                         Plan* best) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (known[dev & 63][0].load(std::memory_order_relaxed) == 0) {
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess) return e;
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+      return e;
     known[dev & 63][0].store(1, std::memory_order_relaxed);
   }
   const int slabs = (a.C + 4 * lanes - 1) / (4 * lanes);
   const int64_t total = (int64_t)a.B * slabs, per_block = kThreads / lanes * run;
   for (int size = 1; size <= kMaxCluster && (size == 1 || (size - 1) * per_block < g.T); ++size) {
     const int64_t at_once = resident_clusters(k, size, smem, known[dev & 63]);
+    if (at_once == 0) continue;
     const int64_t waves = (total + at_once - 1) / at_once, rounds = (g.T + size * per_block - 1) / (size * per_block);
     const float sharing = (float)(std::min(total, at_once) * size) / 148.f;
-    const float round = lanes == 8 ? 2.2f + 0.45f * sharing : 2.3f + 0.55f * sharing;
+    const float round = (lanes == 8 ? 2.2f + 0.45f * sharing : 2.3f + 0.55f * sharing) + 0.12f * std::max(0, size - 8);
     const float cost = (float)waves * (float)(rounds + 2) * round;
     if (cost < best->cost) *best = Plan{k, lanes, slabs, size, (int)rounds, cost};
   }

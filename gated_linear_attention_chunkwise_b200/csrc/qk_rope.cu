@@ -17,6 +17,7 @@
 #include <math.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "four.cuh"
 #include "internal.h"
@@ -175,10 +176,19 @@ __device__ __forceinline__ uint2 again(uint2 v) {
 __device__ __forceinline__ float4 again(float4 v) { return v; }
 
 // ---- forward ------------------------------------------------------------------------------
+// A number of heads known at compile time, for the loops over the heads in flight.
+template <int n>
+using Count = std::integral_constant<int, n>;
+
+// Blocks an SM that the registers allow without spilling much.
+template <typename T>
+constexpr int resident(bool norm) {
+  return sizeof(T) == 2 ? 6 : norm ? 4 : 5;
+}
+
 template <typename T, bool kNorm, bool kInter>
-__global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) {
+__global__ void __launch_bounds__(kThreads, resident<T>(kNorm)) qk_rope_k(QkRopeArgs a, Split w) {
   using Raw = typename Four<T>::Raw;
-  constexpr int kHeads = 4;  // in flight
   __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
   const int warp = threadIdx.x >> 5;
   const int64_t item = (int64_t)blockIdx.x * kWarps + warp;
@@ -187,42 +197,90 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
   const int part = (int)(item - row * w.parts);
   const long long pos = position(a, row);
   const Lane<kInter> at(a, w.lanes);
-  Raw ra[kHeads], rb[kHeads];
+  const float inv_d = 1.f / a.D;
   const int to_b = at.b - at.a, next = at.groups * a.D;  // from quad to quad, from step to step
+  Raw ra[4], rb[4];
   const T* in;
-  int head, end;  // this lane's head, and what it is below
+  T* out;
+  int left, room;  // steps left; elements from this lane's head to the last one of the row
   auto start = [&](const HeadRows& t, int from, int to) {
-    head = from * at.groups + at.group;
-    end = at.on ? min(to * at.groups, t.H) : 0;
-    in = static_cast<const T*>(t.in) + row * t.stride + (int64_t)head * a.D + at.a;
+    const int head = from * at.groups + at.group;
+    const int64_t off = (int64_t)head * a.D + at.a;
+    in = static_cast<const T*>(t.in) + row * t.stride + off;
+    out = static_cast<T*>(t.out) + row * t.out_stride + off;
+    left = to - from;
+    room = (t.H - 1 - head) * a.D;
   };
-  auto load = [&] {
+  auto load = [&](auto n) {  // a lane behind the last head reads the last head
 #pragma unroll
-    for (int k = 0; k < kHeads; ++k) {
-      ra[k] = rb[k] = Raw{};
-      if (head + k * at.groups < end) {
-        ra[k] = *reinterpret_cast<const Raw*>(in + k * next);
-        rb[k] = *reinterpret_cast<const Raw*>(in + k * next + to_b);
-      }
+    for (int k = 0; k < n(); ++k) {
+      const T* p = in + min(k * next, room);
+      ra[k] = *reinterpret_cast<const Raw*>(p);
+      rb[k] = *reinterpret_cast<const Raw*>(p + to_b);
     }
-    in += kHeads * next;
+  };
+  Mix turn;  // xc, yc: the weights alone where nothing turns
+  auto finish = [&](auto n) {
+    float r[n()];
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int k = 0; k < n(); ++k) {
+        const F4 x = Four<T>::get(ra[k]), y = Four<T>::get(rb[k]);
+        r[k] = sum4(fma4(y, y, mul4(x, x)));
+        ra[k] = again(ra[k]);
+        rb[k] = again(rb[k]);
+      }
+      group_sum(r, at.g);
+#pragma unroll
+      for (int k = 0; k < n(); ++k) r[k] = rsqrtf(fmaf(r[k], inv_d, a.eps));
+    }
+#pragma unroll
+    for (int k = 0; k < n(); ++k) {
+      if (!at.on || k * next > room) continue;
+      T* const oa = out + k * next;
+      if (!kNorm && !at.turned) {  // a copy
+        *reinterpret_cast<Raw*>(oa) = ra[k];
+        *reinterpret_cast<Raw*>(oa + to_b) = rb[k];
+        continue;
+      }
+      Pairs p = as_pairs<kInter>(Four<T>::get(ra[k]), Four<T>::get(rb[k]));
+      if constexpr (kNorm) p = scaled(p, r[k]);
+      p = at.turned ? mix(p, turn) : Pairs{mul4(p.x, turn.xc), mul4(p.y, turn.yc)};
+      F4 x, y;
+      as_quads<kInter>(p, x, y);
+      store4(oa, x);
+      store4(oa + to_b, y);
+    }
+    in += n() * next;
+    out += n() * next;
+    room -= n() * next;
+    left -= n();
   };
   int from, to;
   share(w, part, 0, from, to);
   int which = from < to ? 0 : 1;  // the share may lie in k alone
   if (which) share(w, part, 1, from, to);
   start(which ? a.k : a.q, from, to);
-  load();  // the first heads travel while the angles are computed
+  // The first heads travel while the angles are computed.
+  if (left >= 4)
+    load(Count<4>());
+  else
+    load(Count<1>());
   angles(a, pos, cs[warp]);
   __syncwarp();
 #pragma unroll 1
-  for (bool loaded = true; which < 2; ++which) {
+  for (bool first = true; which < 2; ++which, first = false) {
     const HeadRows& t = which ? a.k : a.q;
-    share(w, part, which, from, to);
-    if (from >= to) continue;
-    if (!loaded) start(t, from, to);
-    T* out = static_cast<T*>(t.out) + row * t.out_stride + (int64_t)head * a.D + at.a;
-    Mix turn{all4(1.f), all4(0.f), all4(1.f), all4(0.f)};  // xc, yc: the weights alone where nothing turns
+    if (!first) {
+      share(w, part, which, from, to);
+      if (from >= to) break;
+      start(t, from, to);
+      if (left >= 4)
+        load(Count<4>());
+      else
+        load(Count<1>());
+    }
+    turn = Mix{all4(1.f), all4(0.f), all4(1.f), all4(0.f)};
     if (at.turned) {
       const Turn f = turn_of(cs[warp] + at.pair);
       turn = Mix{f.c, f.s, f.c, minus(f.s)};
@@ -231,43 +289,24 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
       const Pairs g = as_pairs<kInter>(load4(t.weight + at.a), load4(t.weight + at.b));
       turn = Mix{mul4(turn.xc, g.x), mul4(turn.xs, g.x), mul4(turn.yc, g.y), mul4(turn.ys, g.y)};
     }
-#pragma unroll 1
-    for (int step = from; step < to; step += kHeads) {
-      if (!loaded) load();
-      loaded = false;
-      float r[kHeads];
-      if constexpr (kNorm) {
-#pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-          const F4 x = Four<T>::get(ra[k]), y = Four<T>::get(rb[k]);
-          r[k] = sum4(fma4(y, y, mul4(x, x)));
-          ra[k] = again(ra[k]);
-          rb[k] = again(rb[k]);
-        }
-        group_sum(r, at.g);
-#pragma unroll
-        for (int k = 0; k < kHeads; ++k) r[k] = rsqrtf(r[k] / a.D + a.eps);
+    // Four heads a group at a time, then two, then one (which is loaded already where it is all).
+    if (left >= 4) {
+      finish(Count<4>());
+      while (left >= 4) {
+        load(Count<4>());
+        finish(Count<4>());
       }
-#pragma unroll
-      for (int k = 0; k < kHeads; ++k) {
-        if (head + k * at.groups >= end) continue;
-        T* const oa = out + k * next;
-        if (!kNorm && !at.turned) {  // a copy
-          *reinterpret_cast<Raw*>(oa) = ra[k];
-          *reinterpret_cast<Raw*>(oa + to_b) = rb[k];
-          continue;
-        }
-        Pairs p = as_pairs<kInter>(Four<T>::get(ra[k]), Four<T>::get(rb[k]));
-        if constexpr (kNorm) p = scaled(p, r[k]);
-        p = at.turned ? mix(p, turn) : Pairs{mul4(p.x, turn.xc), mul4(p.y, turn.yc)};
-        F4 x, y;
-        as_quads<kInter>(p, x, y);
-        store4(oa, x);
-        store4(oa + to_b, y);
+      if (left >= 2) {
+        load(Count<2>());
+        finish(Count<2>());
       }
-      head += kHeads * at.groups;
-      out += kHeads * next;
+      if (left) load(Count<1>());
+    } else if (left >= 2) {
+      load(Count<2>());
+      finish(Count<2>());
+      if (left) load(Count<1>());
     }
+    if (left) finish(Count<1>());
   }
 }
 
@@ -277,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 6) qk_rope_k(QkRopeArgs a, Split w) 
 template <typename T, bool kInter>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, Split w, float* part_sums) {
   using Raw = typename Four<T>::Raw;
-  constexpr int kHeads = 2;  // in flight
   __shared__ __align__(16) float2 cs[kWarps][kMaxPairs];
   __shared__ __align__(16) float sums[kWarps][2][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -308,61 +346,58 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, 
       share(w, part, which, from, to);
       if (from >= to) continue;
       const Pairs weight = as_pairs<kInter>(load4(t.weight + at.a), load4(t.weight + at.b));
-      int head = from * at.groups + at.group;
-      const int64_t off = (int64_t)head * a.D + at.a;
+      const int first = from * at.groups + at.group;
+      const int64_t off = (int64_t)first * a.D + at.a;
       const T* in = static_cast<const T*>(t.in) + row * t.stride + off;
       const T* grad = static_cast<const T*>(t.grad) + row * t.grad_stride + off;
       T* out = static_cast<T*>(t.out) + row * t.out_stride + off;
-      const int end = at.on ? min(to * at.groups, t.H) : 0;  // this lane's heads are below it
-#pragma unroll 1
-      for (int step = from; step < to; step += kHeads) {
-        Raw xa[kHeads], xb[kHeads], ga[kHeads], gb[kHeads];
+      int room = (t.H - 1 - first) * a.D;  // elements from this lane's head to the last one of the row
+      auto heads = [&](auto n) {
+        Raw xa[n()], xb[n()];
+        Pairs turned[n()];
+        float sd[2 * n()];
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-          xa[k] = xb[k] = ga[k] = gb[k] = Raw{};
-          if (head + k * at.groups < end) {
-            xa[k] = *reinterpret_cast<const Raw*>(in + k * next);
-            xb[k] = *reinterpret_cast<const Raw*>(in + k * next + to_b);
-            ga[k] = *reinterpret_cast<const Raw*>(grad + k * next);
-            gb[k] = *reinterpret_cast<const Raw*>(grad + k * next + to_b);
-          }
+        for (int k = 0; k < n(); ++k) {  // a lane behind the last head reads the last head
+          const int o = min(k * next, room);
+          xa[k] = *reinterpret_cast<const Raw*>(in + o);
+          xb[k] = *reinterpret_cast<const Raw*>(in + o + to_b);
+          turned[k] = as_pairs<kInter>(load4(grad + o), load4(grad + o + to_b));
         }
-        float sd[2 * kHeads];
-        Pairs turned[kHeads];
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
+        for (int k = 0; k < n(); ++k) {
           const Pairs x = as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k]));
-          Pairs g = as_pairs<kInter>(Four<T>::get(ga[k]), Four<T>::get(gb[k]));
-          if (at.turned) g = mix(g, back);
-          turned[k] = g;
+          if (at.turned) turned[k] = mix(turned[k], back);
           const Pairs wx = times(x, weight);
           sd[2 * k] = sum4(fma4(x.y, x.y, mul4(x.x, x.x)));
-          sd[2 * k + 1] = sum4(fma4(wx.y, g.y, mul4(wx.x, g.x)));
+          sd[2 * k + 1] = sum4(fma4(wx.y, turned[k].y, mul4(wx.x, turned[k].x)));
           xa[k] = again(xa[k]);
           xb[k] = again(xb[k]);
         }
         group_sum(sd, at.g);
 #pragma unroll
-        for (int k = 0; k < kHeads; ++k) {
-          if (head + k * at.groups >= end) continue;
-          const float r = rsqrtf(sd[2 * k] * inv_d + a.eps);
+        for (int k = 0; k < n(); ++k) {
+          if (!at.on || k * next > room) continue;
+          const float r = rsqrtf(fmaf(sd[2 * k], inv_d, a.eps));
           const float m = sd[2 * k + 1] * r * inv_d;
-          const Pairs g = turned[k];
-          const Pairs n = scaled(as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k])), r);
-          dw[which] = Pairs{fma4(g.x, n.x, dw[which].x), fma4(g.y, n.y, dw[which].y)};
+          const Pairs& g = turned[k];
+          const Pairs n_ = scaled(as_pairs<kInter>(Four<T>::get(xa[k]), Four<T>::get(xb[k])), r);
+          dw[which] = Pairs{fma4(g.x, n_.x, dw[which].x), fma4(g.y, n_.y, dw[which].y)};
           // r (w g - m n)
           const Pairs wg = times(scaled(g, r), weight);
           const F4 mr = all4(-m * r);
           F4 p, q;
-          as_quads<kInter>(Pairs{fma4(n.x, mr, wg.x), fma4(n.y, mr, wg.y)}, p, q);
+          as_quads<kInter>(Pairs{fma4(n_.x, mr, wg.x), fma4(n_.y, mr, wg.y)}, p, q);
           store4(out + k * next, p);
           store4(out + k * next + to_b, q);
         }
-        head += kHeads * at.groups;
-        in += kHeads * next;
-        grad += kHeads * next;
-        out += kHeads * next;
-      }
+        in += n() * next;
+        grad += n() * next;
+        out += n() * next;
+        room -= n() * next;
+      };
+      int left = to - from;
+      for (; left >= 2; left -= 2) heads(Count<2>());
+      if (left) heads(Count<1>());
     }
   }
   // The warp's heads in order (a head's lanes hold the same channels), then the warps.

@@ -1,6 +1,10 @@
 // glr_bwd.cu -- the gradients of the gated linear recurrence (include/dig_gla.h, glr_bwd,
 // glr_bwd_packed): the walk of glr_scan.cuh from the last token to the first.  Position j of
 // the walk is scan position T - 1 - j; what enters a span is r of the token behind it.
+//
+// Four tokens a thread, since a token needs four values a channel (alpha, d and the two
+// factors of the gradients): packed 32749 x 2048, logits and complement, 310 us; eight tokens
+// and two blocks an SM 314, four and four blocks (spilling) 349.
 #include "glr_scan.cuh"
 
 namespace dig {

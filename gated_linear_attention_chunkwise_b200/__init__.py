@@ -373,8 +373,8 @@ def _gated(x, gate, gate_norm, dims: int):
         norm, gtype = 0.0, torch.float32
     else:
         norm, gtype = float(gate_norm), dtype
-        if not 0.0 < norm < math.inf:
-            raise ValueError("gate_norm must be positive and finite (None: gate holds log_alpha)")
+        if not 1e-30 <= norm <= 1e38:  # as fp32, where 0 would mean log_alpha
+            raise ValueError("gate_norm must be in [1e-30, 1e38] (None: gate holds log_alpha)")
     _on(gate, "gate", gtype, dev, index)
     if len(shape) != dims or gate.shape != shape:
         raise ValueError(f"expected x and gate of the same {dims}-dimensional shape")

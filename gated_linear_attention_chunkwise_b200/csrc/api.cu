@@ -23,9 +23,12 @@ __device__ int g_device_status = 0;
 namespace {
 
 std::mutex g_mu;
+std::atomic<int> g_setup{1};
 int g_arch_ok[64];  // per device: 0 unknown, 1 sm_100, -1 other
 
 }  // namespace
+
+int setup_generation() { return g_setup.load(std::memory_order_relaxed); }
 
 int check_device() {
   int dev = 0;
@@ -513,6 +516,7 @@ void dig_gla_test_skip_items(int n) { dig::g_test_skip.store(n > 0 ? n : 0); }
 void dig_gla_release(void) {
   {
     std::lock_guard<std::mutex> lk(dig::g_mu);
+    dig::g_setup.fetch_add(1);
     memset(dig::g_arch_ok, 0, sizeof(dig::g_arch_ok));
     for (cudaMemPool_t& p : dig::g_pool) {
       // Allocations still in flight keep their memory until they are freed; the

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
 #pragma unroll
       for (int i = 0; i < kRun; ++i) s = Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
     }
-    bool odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
-    if (n < kRun || odd) {  // the last round's end, growth, values that are not finite
+    bool odd = !all_within(s.A, 1.f) || (packed && !modest(s.h));
+    if (n < kRun || odd) {  // the last round's end, growth, values that may not stay finite
       s = nothing();
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
         if (m.last >> i & 1u) s = Span{all4(0.f), all4(0.f)};
         s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), mul4(al[i], add4(d[i], s.h))};
       }
-      odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
+      odd = !all_within(s.A, 1.f) || (packed && !modest(s.h));
     }
     if (m.last) s.A.a.x = -0.f;
     F4 r;

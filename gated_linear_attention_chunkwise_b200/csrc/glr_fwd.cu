@@ -109,8 +109,8 @@ __global__ void __launch_bounds__(kThreads, resident(kKind, kComp))
     Span s{al[0], u[0]};
 #pragma unroll
     for (int i = 1; i < kRun; ++i) s = Span{mul4(s.A, al[i]), fma4(al[i], s.h, u[i])};
-    bool odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
-    if (n < kRun || odd) {  // the last round's end, growth, values that are not finite
+    bool odd = !all_within(s.A, 1.f) || (packed && !modest(s.h));
+    if (n < kRun || odd) {  // the last round's end, growth, values that may not stay finite
       s = nothing();
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads, resident(kKind, kComp))
         else
           s = Span{capped(mul4(s.A, capped(al[i], grown)), grown), fma4(al[i], s.h, u[i])};
       }
-      odd = !all_within(s.A, 1.f) || (packed && !finite4(s.h));
+      odd = !all_within(s.A, 1.f) || (packed && !modest(s.h));
     }
     if (m.first) s.A.a.x = -0.f;
     F4 h;

@@ -72,9 +72,9 @@ __device__ __forceinline__ bool any_over(F4 v, float most) {  // (a NaN compares
 __device__ __forceinline__ bool all_within(F4 v, float most) {  // (a NaN compares false)
   return v.a.x <= most && v.a.y <= most && v.b.x <= most && v.b.y <= most;
 }
-__device__ __forceinline__ bool finite4(F4 v) {
-  const float2 s = __fmul2_rn(__fadd2_rn(v.a, v.b), both(0.f));
-  return s.x + s.y == 0.f;  // (sums that overflow count as not finite)
+// Values whose sums over a block's spans stay finite (a NaN compares false).
+__device__ __forceinline__ bool modest(F4 v) {
+  return fabsf(v.a.x) <= 1e30f && fabsf(v.a.y) <= 1e30f && fabsf(v.b.x) <= 1e30f && fabsf(v.b.y) <= 1e30f;
 }
 // Growth is held at the largest fp32 number (and reported), so that a zero that enters
 // later gives zero instead of NaN.
@@ -155,8 +155,8 @@ struct Walk {
   }
 
   // The value that enters this thread's span s.  Returns false, in all threads of the block
-  // alike, when the wait for the other blocks ran out.  odd: s is not finite or its A may
-  // exceed 1 (otherwise no product of spans overflows, and A = 0 forgets).  marks: spans of
+  // alike, when the wait for the other blocks ran out.  odd: s is not modest or its A may
+  // exceed 1 (otherwise no join of spans overflows, and A = 0 forgets).  marks: spans of
   // the slab may be marked.  meanwhile() runs while the totals travel: the next round's copies
   // and searches.
   //
@@ -421,7 +421,7 @@ inline int resident_clusters(Kernel k, int size, size_t smem, std::atomic<int>* 
 }
 
 // `known`: a table of the kernel's own, [device][cluster size], for the figures above; [device][0]:
-// its shared memory is set up.
+// the setup that its attributes were made in.
 using Known = std::atomic<int>[64][kMaxCluster + 1];
 
 // How to launch one kernel: clusters of `cluster` blocks over slabs of 4 * lanes channels.
@@ -444,11 +444,12 @@ inline cudaError_t plan(Kernel k, Known& known, const GlrArgs& a, const ScanGeom
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (known[dev & 63][0].load(std::memory_order_relaxed) == 0) {
+  const int setup = setup_generation();
+  if (known[dev & 63][0].load(std::memory_order_relaxed) != setup) {
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) != cudaSuccess ||
         (e = cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
       return e;
-    known[dev & 63][0].store(1, std::memory_order_relaxed);
+    known[dev & 63][0].store(setup, std::memory_order_relaxed);
   }
   const int slabs = (a.C + 4 * lanes - 1) / (4 * lanes);
   const int64_t total = (int64_t)a.B * slabs, per_block = kThreads / lanes * run;

@@ -126,6 +126,8 @@ cudaError_t qk_norm_rope_bwd_launch(const QkRopeArgs& a, void* workspace, cudaSt
 int take_test_skip_items();
 
 // ---- host checks shared by the entry points (api.cu) ----
+// Changes with every dig_gla_release(): kernel attributes set in an earlier one may be gone.
+int setup_generation();
 // GLA_OK when the current device is an sm_100 part (cached per device).
 int check_device();
 // Argument validation of a GLA call with q/k/v/out elements of `elt` bytes.

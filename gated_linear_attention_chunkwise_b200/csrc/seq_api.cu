@@ -37,7 +37,7 @@ int check_glr_shape(int64_t rows, int64_t nseq, int C, int64_t x_stride, int64_t
                     int complement, int dtype) {
   if (rows <= 0 || nseq <= 0 || C <= 0) return GLA_ERR_INVALID_ARG;
   if (dtype != GLA_BF16 && dtype != GLA_F32) return GLA_ERR_INVALID_ARG;
-  if (!(gate_norm >= 0.f) || std::isinf(gate_norm) || (complement != 0 && complement != 1)) return GLA_ERR_INVALID_ARG;
+  if (!(gate_norm == 0.f || gate_norm >= 1e-30f) || std::isinf(gate_norm) || (complement != 0 && complement != 1)) return GLA_ERR_INVALID_ARG;
   if (x_stride < C || gate_stride < C) return GLA_ERR_INVALID_ARG;
   const int64_t elt = dtype == GLA_BF16 ? 2 : 4, gelt = gate_norm == 0.f ? 4 : elt;
   if (C > 65536 || nseq > (1 << 24) || nseq * ((C + 63) / 64) > (int64_t)1 << 26) return GLA_ERR_UNSUPPORTED;

@@ -255,7 +255,7 @@ int dwconv3x3(const void* x, const float* w, int B, int Hgrid, int Wgrid, int C,
  *   x         rows of C channels of `dtype`; consecutive token rows are x_stride elements
  *             apart (x_stride >= C: a slice of a wider projection), batches follow one
  *             another without a gap.
- *   gate      gate_norm = 0: log_alpha, fp32.  gate_norm > 0: logits of `dtype`,
+ *   gate      gate_norm = 0: log_alpha, fp32.  gate_norm >= 1e-30: logits of `dtype`,
  *             log_alpha = logsigmoid(gate) / gate_norm (as gla_fwd_glogit).  Rows
  *             gate_stride elements apart.
  *   h0        fp32 [sequences][C], the state before the first token; NULL: zero.
@@ -336,8 +336,8 @@ int glr_step(const void* x, const void* gate, const float* state, const int* slo
  *             k = NULL with Hk = 0: queries alone.
  *   positions DEVICE int32 [rows] (positions64 = 0) or int64 (1), of any sign and size; NULL:
  *             row r has position r mod period (rows of sequences of `period` tokens).
- *   inv_freq  fp32 [rot / 2].  The angle is formed in fp64, so the phase of a far
- *             position is that of the exact product.
+ *   inv_freq  fp32 [rot / 2].  The angle is formed in fp64: the phase of a far position is
+ *             that of the exact product to within 2^-51 of the turns it makes.
  *   q_out, k_out  rows like q and k with strides of their own; each may be its input (same
  *             pointer and stride), and overlaps no input otherwise.
  * D and rot are multiples of 8, 8 <= rot <= D <= 256; pointers and row strides are

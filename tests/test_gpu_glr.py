@@ -455,6 +455,36 @@ def test_a_nan_ends_with_its_sequence(dig, reverse):
     assert dig.device_status() == 0
 
 
+@pytest.mark.parametrize("value", [3e37, float("inf"), 1e25])
+def test_an_overflow_ends_with_its_sequence(dig, value):
+    """Values that overflow inside one sequence leave the others as they were."""
+    rows, C = 700, 64
+    cu = [0, 90, 333, 350, 700]
+    dcu = torch.tensor(cu, dtype=torch.int32).cuda()
+    x, gate = inputs(36, (rows,), C, torch.float32, None)
+    out, last = dig.glr_fwd_packed(x, gate, dcu)
+    bad = x.clone()
+    bad[90:333] = value
+    o, l = dig.glr_fwd_packed(bad, gate, dcu)
+    dx, dg, dh0 = dig.glr_bwd_packed(x, gate, out, x, dcu)
+    px, pg, p0 = dig.glr_bwd_packed(x, gate, out, bad, dcu)
+    for s in (slice(0, 90), slice(333, 700)):
+        for p, q in ((o, out), (px, dx), (pg, dg)):
+            assert torch.allclose(p[s], q[s], rtol=1e-5, atol=1e-6)
+    assert torch.allclose(l[[0, 2, 3]], last[[0, 2, 3]], rtol=1e-5, atol=1e-6)
+    assert torch.allclose(p0[[0, 2, 3]], dh0[[0, 2, 3]], rtol=1e-5, atol=1e-6)
+
+
+def test_after_release(dig):
+    """dig_gla_release forgets what was set up; wide clusters and the workspace come back."""
+    x, gate = inputs(37, (1, 9000), 64, torch.bfloat16, 16.0)
+    want = dig.glr_fwd(x, gate, 1, 9000, 0, gate_norm=16.0)
+    torch.cuda.synchronize()
+    dig.lib().dig_gla_release()
+    got = dig.glr_fwd(x, gate, 1, 9000, 0, gate_norm=16.0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and dig.device_status() == 0
+
+
 def test_two_calls_at_once(dig):
     """Long and short calls on two streams at the same time, each with its own results."""
     xs = [inputs(40 + i, (1, T), 512, torch.bfloat16, 16.0) for i, T in enumerate((20000, 700))]

@@ -60,7 +60,7 @@ def test_glr_shapes(lib, call):
     else:
         assert call(lib, B=0) == INVALID
         assert call(lib, Hg=1 << 16, Wg=1 << 16) == UNSUPPORTED
-    assert call(lib, norm=-1.0) == INVALID
+    assert call(lib, norm=-1.0) == INVALID and call(lib, norm=1e-31) == INVALID
     assert call(lib, norm=float("nan")) == INVALID and call(lib, norm=float("inf")) == INVALID
     assert call(lib, comp=2) == INVALID
     assert call(lib, dt=2) == INVALID
@@ -185,6 +185,9 @@ def test_binding_refuses_cpu_tensors_and_shapes():
         dig.glr_fwd(x.half(), x, 1, 4, 0)
     with pytest.raises(TypeError):
         dig.glr_step(None, x, x)
+    for norm in (0.0, -1.0, 1e-50, 1e39, float("nan")):   # 1e-50 would be 0 as fp32: log_alpha
+        with pytest.raises(ValueError):
+            dig.glr_fwd(x, x, 1, 4, 0, gate_norm=norm)
     with pytest.raises(TypeError):
         dig.rope(None, None, None, x)
     with pytest.raises(TypeError):

@@ -25,6 +25,7 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17", "-rdc=true",
     "-Xcompiler", "-fPIC", "-shared",
     "--expt-relaxed-constexpr",
+    "--threads", "0",  # the sources side by side
 ]
 
 

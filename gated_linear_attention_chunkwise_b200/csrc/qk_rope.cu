@@ -10,7 +10,7 @@
 // 128: 58 us), with the norm 73 % (70 us), of fp32 heads 77 % (8191 tokens of 32 heads of 80:
 // 33 us) and 86 %.  What keeps the norm from more is instruction issue (64 % of the cycles:
 // unpacking, two passes over a head's channels around the sum, the packing).  The gradient
-// reaches 42 % with 72 channels and 60 % with 128 (25088 tokens of 32 heads of 72: 125 us):
+// reaches 42 % with 72 channels and 60 % with 128 (25088 tokens of 32 heads of 72: 124 us):
 // twice the work of a head, 16 warps an SM, 27 of 32 lanes at 72 channels.
 //
 // Split.  Eight channels that rotate among themselves are a unit: quads i and i + rot / 8
@@ -376,8 +376,6 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_bwd_k(QkRopeArgs a, 
           const Pairs wx = times(x, weight);
           sd[2 * k] = sum4(fma4(x.y, x.y, mul4(x.x, x.x)));
           sd[2 * k + 1] = sum4(fma4(wx.y, turned[k].y, mul4(wx.x, turned[k].x)));
-          xa[k] = again(xa[k]);
-          xb[k] = again(xb[k]);
         }
         group_sum(sd, at.g);
 #pragma unroll

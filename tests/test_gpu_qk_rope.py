@@ -178,6 +178,11 @@ def test_repeats_streams_and_graphs(dig):
         again = all_of()
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(again, want))
+    side.wait_stream(torch.cuda.current_stream())
+    given = [dig.qk_norm_rope_bwd(dq, dk, q, k, w, w, pos, inv, stream=side) for _ in range(3)]
+    side.synchronize()
+    for got in given:
+        assert all(torch.equal(a, b) for a, b in zip(got, want[4:]))
     graphs = []
     for _ in range(2):
         g = torch.cuda.CUDAGraph()

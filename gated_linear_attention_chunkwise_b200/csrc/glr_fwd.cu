@@ -18,7 +18,7 @@ __global__ void __launch_bounds__(kThreads, resident(kKind, kComp))
   using RawT = typename Four<T>::Raw;
   using RawG = typename Four<G>::Raw;
   __shared__ Shared<kLanes> sm;
-  extern __shared__ uint4 slots[];  // this round's tokens: gates [kRun][kThreads], then x
+  extern __shared__ uint4 slots[];  // the tokens of a round: gates [kRun][kThreads], then x
   RawG* const sg = reinterpret_cast<RawG*>(slots) + threadIdx.x;
   RawT* const sx = reinterpret_cast<RawT*>(reinterpret_cast<RawG*>(slots) + kRun * kThreads) + threadIdx.x;
 

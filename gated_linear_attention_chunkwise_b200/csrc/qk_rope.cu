@@ -17,9 +17,9 @@
 // of the head when pairs are half a span apart, two adjacent quads when they are interleaved
 // or not rotated.  D / 8 lanes hold a head in registers, a unit each, and sum its squares by
 // shuffles; a warp holds as many heads at once as fit (72 channels: three heads on 27 lanes)
-// and walks the heads of one token, four in flight (two: prompt 74 -> 82 us; six: 78).  It computes the token's angles once,
-// one pair a lane, and keeps cos and sin in shared memory.  With few tokens a token's heads
-// are shared between warps.
+// and walks the heads of one token, four in flight (two: prompt 74 -> 82 us; six: 78).  It
+// computes the token's angles once, one pair a lane, and keeps cos and sin in shared memory.
+// With few tokens a token's heads are shared between warps.
 #include <math.h>
 
 #include <algorithm>
@@ -97,7 +97,6 @@ __device__ __forceinline__ Pairs mix(const Pairs& p, const Mix& t) {
 }
 __device__ __forceinline__ Pairs times(const Pairs& p, const Pairs& q) { return Pairs{mul4(p.x, q.x), mul4(p.y, q.y)}; }
 __device__ __forceinline__ Pairs scaled(const Pairs& p, float f) { return Pairs{mul4(p.x, all4(f)), mul4(p.y, all4(f))}; }
-__device__ __forceinline__ F4 dot4(const Pairs& p, const Pairs& q, F4 sum) { return fma4(p.y, q.y, fma4(p.x, q.x, sum)); }
 __device__ __forceinline__ float sum4(F4 v) {
   const float2 s = __fadd2_rn(v.a, v.b);
   return s.x + s.y;

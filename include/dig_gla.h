@@ -352,7 +352,8 @@ int rope(const void* q, const void* k, const void* positions, int positions64, i
  * qk_norm_rope -- the RMS norm of every query and key head, then rope, in one pass:
  *     y = x / sqrt(mean(x^2) + eps) * weight   over the D channels of a head,   out = rope(y)
  *   q_weight, k_weight  fp32 [D].  rot = 0 (inv_freq NULL): the norm alone.
- * The rest as rope.  Arithmetic is fp32, rounded once at the end.
+ * The rest as rope.  Arithmetic is fp32 (squares of channels above 1e18 overflow it), rounded
+ * once at the end.
  */
 int qk_norm_rope(const void* q, const void* k, const float* q_weight, const float* k_weight, const void* positions,
                  int positions64, int period, const float* inv_freq, int64_t rows, int Hq, int Hk, int D, int rot,

@@ -26,7 +26,7 @@
 // the latency of a round's exchange.  Eight tokens a thread: with 4 the fixed work of a round
 // (330 instructions a thread) doubles an element (one 16384 x 2048 call 68 -> 86 us), with 16
 // the registers leave too few warps (packed, logits: 341 -> 373 us).  128 threads a block:
-// 64 take 385 us there, 256 take 377 us.
+// 64 take 385 us there, 96 take 348, 160 take 393, 256 take 377.
 #pragma once
 
 #include <algorithm>

@@ -352,7 +352,7 @@ __device__ __forceinline__ Marks mark(const GlrArgs& a, int lo, int n, bool turn
   const int end = lo + n;
   m.inside = 0u;
   int s = q < 0 ? 0 : a.cu[q], e = q < 0 ? a.cu[0] : a.cu[q + 1];
-  at = Amid{s, e, q};
+  at = q < 0 ? Amid{} : Amid{s, e, q};  // the rows before all sequences lie in none
   while (true) {  // one sequence after another
     const int from = max(s, lo), to = min(e, end);
     if (q >= 0 && from < to) {

@@ -121,6 +121,15 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
       }
       pull[i] = kKind == kGateLog ? before : mul4(before, k.slope);
     }
+    // Rows of no sequence pass on what enters them, whatever they hold.
+    if (packed && m.inside != (1u << kRun) - 1u) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (m.inside >> i & 1u) continue;
+        al[i] = all4(1.f);
+        d[i] = all4(0.f);
+      }
+    }
     // The last token of a sequence takes dh_last in and forgets the token behind.
     Span s = nothing();
     if (m.last) {

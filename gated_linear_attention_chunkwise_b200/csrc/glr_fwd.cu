@@ -94,6 +94,15 @@ __global__ void __launch_bounds__(kThreads, resident(kKind, kComp))
       if constexpr (kComp) u[i] = mul4(k.rest, u[i]);
       al[i] = k.alpha;
     }
+    // Rows of no sequence pass on what enters them, whatever they hold.
+    if (packed && m.inside != (1u << kRun) - 1u) {
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) {
+        if (m.inside >> i & 1u) continue;
+        al[i] = all4(1.f);
+        u[i] = all4(0.f);
+      }
+    }
     // The first token of a sequence takes its state in and forgets the token before.
     if (m.first) {
 #pragma unroll

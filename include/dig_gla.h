@@ -281,8 +281,8 @@ int glr_fwd(const void* x, const void* gate, const float* h0, int B, int Hgrid, 
  * glr_fwd_packed -- the same over packed sequences of different lengths: sequence n is
  * the rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 (DEVICE int32 [nseq + 1], ascending from
  * >= 0 to <= rows; empty sequences allowed), scanned forwards (dir = 0) or backwards
- * (dir = 1).  Rows of no sequence (padding): fill = 0 leaves their outputs as they were,
- * fill = 1 writes zeros.  A cu_seqlens that is not ascending or leaves [0, rows] is
+ * (dir = 1).  Rows of no sequence (padding), whatever they hold, change neither a sequence nor
+ * the device status: fill = 0 leaves their outputs as they were, fill = 1 writes zeros.  A cu_seqlens that is not ascending or leaves [0, rows] is
  * recorded as GLA_ERR_INVALID_ARG in the device status, and the outputs are unspecified.
  */
 int glr_fwd_packed(const void* x, const void* gate, const int* cu_seqlens, const float* h0, int64_t rows, int nseq, int C,

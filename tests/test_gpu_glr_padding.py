@@ -42,3 +42,29 @@ def test_gradients_summed_over_all_rows_see_no_padding(dig, d):
         assert bool((t[:7000] == 0).all()) and bool((t[8100:] == 0).all())
         assert bool(torch.isfinite(t.sum(0)).all())
     assert dig.device_status() == 0
+
+
+@pytest.mark.parametrize("d", [0, 1])
+@pytest.mark.parametrize("gap", [70, 3000])
+@pytest.mark.parametrize("junk", [float("inf"), -float("inf"), float("nan"), 3e38, 100.0])
+def test_padding_of_any_value_changes_neither_results_nor_the_status(dig, junk, gap, d):
+    """Bit for bit what the same call gives with zeros in the padding, and no error recorded."""
+    C, cu = 72, [gap, gap + 1, gap + 330, gap + 331, gap + 760]
+    rows = cu[-1] + 513
+    dcu = torch.tensor(cu, dtype=torch.int32).cuda()
+    for gate_norm, comp in ((None, False), (None, True), (1.0, False), (16.0, True)):
+        x, gate = inputs(30, (rows,), C, torch.float32, gate_norm)
+        h0, dout, dlast = normal(31, (4, C)), normal(32, (rows, C)), normal(33, (4, C))
+        clean = [x, gate, dout]
+        for t in clean:
+            t[:gap], t[cu[-1]:] = 0, 0
+        out, last = dig.glr_fwd_packed(x, gate, dcu, d, gate_norm, comp, h0=h0)
+        grads = dig.glr_bwd_packed(x, gate, out, dout, dcu, d, gate_norm, comp, h0=h0, dh_last=dlast)
+        bad = [t.clone() for t in (x, gate, out, dout)]
+        for t in bad:
+            t[:gap], t[cu[-1]:] = junk, junk
+        again = dig.glr_fwd_packed(bad[0], bad[1], dcu, d, gate_norm, comp, h0=h0)
+        more = dig.glr_bwd_packed(*bad, dcu, d, gate_norm, comp, h0=h0, dh_last=dlast)
+        assert dig.device_status() == 0
+        for p, q in zip((out, last, *grads), (*again, *more)):
+            assert torch.equal(p, q)

@@ -39,16 +39,43 @@ __device__ __forceinline__ float rcp_fast(float x) {
 }
 constexpr float kLog2e = 1.4426950408889634f;
 
-// 1 - e^x from x and e^x, without the cancellation of the subtraction near 0: the Taylor
-// polynomial within |x| < 0.15 (remainder 3e-9 of it), where 1 - e^x would lose more than
-// three of the 24 bits.
-__device__ __forceinline__ float2 one_minus_exp(float2 x, float2 ex) {
-  float2 p = __ffma2_rn(x, both(1.f / 720.f), both(1.f / 120.f));
-  p = __ffma2_rn(x, p, both(1.f / 24.f));
+// The exponential behind the logits: 1 - alpha and the gradient inherit its relative error, so
+// calls in fp32 (kFine) take expf; calls in bf16 the hardware's, far below half a step of 2^-9.
+template <bool kFine>
+__device__ __forceinline__ float2 exp_of(float2 x) {
+  if constexpr (kFine) return make_float2(expf(x.x), expf(x.y));
+  const float2 t = __fmul2_rn(x, both(kLog2e));
+  return make_float2(exp2_fast(t.x), exp2_fast(t.y));
+}
+
+// alpha = e^x and, where kRest, 1 - alpha.  Near 0 both come from the Taylor polynomial of
+// e^x - 1: a subtraction would lose the leading bits of 1 - alpha, and the hardware's e^x is off
+// by up to 2^-22 just below 1, an error of the decay that acts again at every token (1.9 units of
+// 2^-24 measured, 0.6 from the polynomial: one rounding).  alpha alone needs three powers within
+// |x| < 1/16 (remainder 8e-9): behind that a state is gone in 16 tokens.  1 - alpha needs five
+// within 0.15 (3e-9 of it); in fp32, where the subtraction would still cost 10 units there, seven
+// within 1/2 (1e-8 of it).
+template <bool kFine, bool kRest>
+__device__ __forceinline__ void decay(float2 x, float2& alpha, float2& rest) {
+  constexpr bool kLong = kFine && kRest;
+  constexpr float kNear = kLong ? 0.5f : kRest ? 0.15f : 0.0625f;
+  const float2 ex = exp_of<false>(x);
+  float2 p = both(kLong ? 1.f / 40320.f : kRest ? 1.f / 720.f : 1.f / 24.f);
+  if constexpr (kLong) {
+    p = __ffma2_rn(x, p, both(1.f / 5040.f));
+    p = __ffma2_rn(x, p, both(1.f / 720.f));
+  }
+  if constexpr (kRest) {
+    p = __ffma2_rn(x, p, both(1.f / 120.f));
+    p = __ffma2_rn(x, p, both(1.f / 24.f));
+  }
   p = __ffma2_rn(x, p, both(1.f / 6.f));
   p = __ffma2_rn(x, p, both(0.5f));
   p = __ffma2_rn(x, p, both(1.f));
-  return make_float2(fabsf(x.x) < 0.15f ? -x.x * p.x : 1.f - ex.x, fabsf(x.y) < 0.15f ? -x.y * p.y : 1.f - ex.y);
+  const float2 close = __ffma2_rn(x, p, both(1.f)), less = __fmul2_rn(x, p), far = __ffma2_rn(ex, both(-1.f), both(1.f));
+  const bool near_x = fabsf(x.x) < kNear, near_y = fabsf(x.y) < kNear;
+  alpha = make_float2(near_x ? close.x : ex.x, near_y ? close.y : ex.y);
+  rest = make_float2(near_x ? -less.x : far.x, near_y ? -less.y : far.y);
 }
 
 // log(1 + e) for e in [0, 1], relative error 2e-7: e times the polynomial that interpolates
@@ -71,27 +98,27 @@ __device__ __forceinline__ float2 log_one_plus(float2 e) {
 struct Gates {
   float2 alpha, rest, slope;
 };
-template <int kKind>
+template <int kKind, bool kFine, bool kRest>
 __device__ __forceinline__ Gates make_gates(float2 g, float inv_norm) {
   Gates r;
   if constexpr (kKind == kGateLog) {
-    r.alpha = make_float2(exp2_fast(g.x * kLog2e), exp2_fast(g.y * kLog2e));
-    r.rest = one_minus_exp(g, r.alpha);
+    decay<kFine, kRest>(g, r.alpha, r.rest);
     r.slope = both(1.f);
   } else {
-    // e = e^{-|g|} never overflows; sigmoid(|g|) = 1 / (1 + e), sigmoid(-|g|) = e / (1 + e).
-    const float2 e = make_float2(exp2_fast(-fabsf(g.x) * kLog2e), exp2_fast(-fabsf(g.y) * kLog2e));
+    // e = e^{-|g|} never overflows; sigmoid(-|g|) = e / (1 + e), sigmoid(|g|) = 1 - that.
+    const float2 e = exp_of<kFine>(make_float2(-fabsf(g.x), -fabsf(g.y)));
     const float2 w = __fadd2_rn(e, both(1.f));
-    const float2 big = make_float2(rcp_fast(w.x), rcp_fast(w.y)), small = __fmul2_rn(e, big);
+    const float2 inv = make_float2(rcp_fast(w.x), rcp_fast(w.y));
+    const float2 small = __fmul2_rn(e, inv), big = __ffma2_rn(small, both(-1.f), both(1.f));
     const float2 off = make_float2(g.x < 0.f ? big.x : small.x, g.y < 0.f ? big.y : small.y);
     if constexpr (kKind == kGateSigmoid) {
       r.alpha = make_float2(g.x < 0.f ? small.x : big.x, g.y < 0.f ? small.y : big.y);
       r.rest = r.slope = off;
     } else {
-      const float2 l = log_one_plus(e);  // carries a NaN that fminf drops
-      const float2 la = make_float2((fminf(g.x, 0.f) - l.x) * inv_norm, (fminf(g.y, 0.f) - l.y) * inv_norm);
-      r.alpha = make_float2(exp2_fast(la.x * kLog2e), exp2_fast(la.y * kLog2e));
-      r.rest = one_minus_exp(la, r.alpha);
+      // (the logarithm carries a NaN that fminf drops)
+      const float2 l = log_one_plus(e);
+      const float2 la = __fmul2_rn(__ffma2_rn(l, both(-1.f), make_float2(fminf(g.x, 0.f), fminf(g.y, 0.f))), both(inv_norm));
+      decay<kFine, kRest>(la, r.alpha, r.rest);
       r.slope = __fmul2_rn(off, both(inv_norm));
     }
   }
@@ -103,9 +130,10 @@ __device__ __forceinline__ Gates make_gates(float2 g, float inv_norm) {
 struct Gates4 {
   F4 alpha, rest, slope;
 };
-template <int kKind>
+template <typename T, int kKind, bool kRest>
 __device__ __forceinline__ Gates4 make_gates4(F4 g, float inv_norm) {
-  const Gates p = make_gates<kKind>(g.a, inv_norm), q = make_gates<kKind>(g.b, inv_norm);
+  constexpr bool kFine = sizeof(T) == 4;
+  const Gates p = make_gates<kKind, kFine, kRest>(g.a, inv_norm), q = make_gates<kKind, kFine, kRest>(g.b, inv_norm);
   return Gates4{F4{p.alpha, q.alpha}, F4{p.rest, q.rest}, F4{p.slope, q.slope}};
 }
 

@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
     auto token = [&](int i) { return a.dir ? j0 + i : g.T - 1 - (j0 + i); };  // of packed rows
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
+      const Gates4 k = make_gates4<T, kKind, kComp>(Four<G>::get(sg[i * kThreads]), inv_norm);
       F4 before = Four<T>::get(sh[i * kThreads]);
       d[i] = Four<T>::get(sd[i * kThreads]);
       al[i] = k.alpha;

@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads, resident(kKind, kComp))
     F4 al[kRun], u[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-      const Gates4 k = make_gates4<kKind>(Four<G>::get(sg[i * kThreads]), inv_norm);
+      const Gates4 k = make_gates4<T, kKind, kComp>(Four<G>::get(sg[i * kThreads]), inv_norm);
       u[i] = Four<T>::get(sx[i * kThreads]);
       if constexpr (kComp) u[i] = mul4(k.rest, u[i]);
       al[i] = k.alpha;

@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) glr_step_k(GlrStepArgs a, int parts)
       g = load4(gate + i * a.gate_stride + c);
     }
     for (int j = i;;) {
-      const Gates4 k = make_gates4<kKind>(g, inv_norm);
+      const Gates4 k = make_gates4<T, kKind, kComp>(g, inv_norm);
       h = fma4(k.alpha, h, kComp ? mul4(k.rest, u) : u);
       store4(out + (int64_t)j * a.C + c, h);
       if (!behind) break;

@@ -530,6 +530,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
       "ramp"    pairs that turn more than beta_fast times over original_length keep their
                 frequency, those that turn less than beta_slow times are divided by
                 factor, in between the two are blended linearly in i; scale = 0.1 ln(factor) + 1
+                (the by-parts interpolation of YaRN, Peng et al. 2023)
     """
     if rot <= 0 or rot % 2:
         raise ValueError("rot must be positive and even")
@@ -553,9 +554,9 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
         def pair_of(turns):  # the (fractional) pair that turns so often over original_length
             return rot * math.log(original_length / (turns * 2 * math.pi)) / (2 * math.log(base))
 
-        low = max(math.floor(pair_of(beta_fast)), 0)
-        high = min(math.ceil(pair_of(beta_slow)), rot // 2 - 1)
-        slow = torch.clamp((i - low) / max(high - low, 1e-3), 0, 1)
+        # Either end may lie outside the table: cut to it, the slope inside would be another.
+        low, high = math.floor(pair_of(beta_fast)), math.ceil(pair_of(beta_slow))
+        slow = torch.clamp((i - low) / max(high - low, 1), 0, 1)
         inv = inv * (1 - slow) + inv / factor * slow
         scale = 0.1 * math.log(factor) + 1.0
     return inv.to(torch.float32).to(device or "cpu"), scale

@@ -559,7 +559,7 @@ def rope_frequencies(rot: int, base: float = 10000.0, scaling: str | None = None
         slow = torch.clamp((i - low) / max(high - low, 1), 0, 1)
         inv = inv * (1 - slow) + inv / factor * slow
         scale = 0.1 * math.log(factor) + 1.0
-    return inv.to(torch.float32).to(device or "cpu"), scale
+    return inv.to(torch.float32).to("cpu" if device is None else device), scale
 
 
 def _heads(t, name: str, dtype, dev, index: int, like):

@@ -47,3 +47,16 @@ def test_a_table_that_ends_inside_the_ramp():
     # (63 - 45) / (70 - 45) of the way: 1 / (0.28 + 0.72 / 8)
     assert divided[63] == pytest.approx(1 / (0.28 + 0.72 / 8), rel=1e-6)
     assert (np.diff(divided) >= -1e-6).all()
+
+
+def test_device_zero_is_a_device():
+    """An index names a CUDA device, 0 among them."""
+    import torch
+    import gated_linear_attention_chunkwise_b200 as dig
+    assert dig.rope_frequencies(8)[0].device.type == "cpu"
+    assert dig.rope_frequencies(8, device="cpu")[0].device.type == "cpu"
+    if torch.cuda.is_available():
+        assert dig.rope_frequencies(8, device=0)[0].device == torch.device("cuda", 0)
+    else:
+        with pytest.raises((RuntimeError, AssertionError)):
+            dig.rope_frequencies(8, device=0)

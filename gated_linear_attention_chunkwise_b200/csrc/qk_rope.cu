@@ -48,15 +48,18 @@ __device__ __forceinline__ long long position(const QkRopeArgs& a, int64_t row) 
 }
 
 // cos and sin of position * inv_freq, times scale.  The angle is formed in fp64, in turns,
-// and reduced there to half a turn, so far positions keep their phase.
+// and reduced there to half a turn, so far positions keep their phase; what fp32 drops of it
+// (6e-8 in radians, all of a sine or cosine near its zero) enters by the first-order term.
 __device__ __forceinline__ void angles(const QkRopeArgs& a, long long position, float2* cs) {
   const double pos = (double)position;
   for (int p = threadIdx.x & 31; p < a.rot / 2; p += 32) {
     double turn = pos * ((double)a.inv_freq[p] * 0.15915494309189535);
     turn -= rint(turn);
     float s, c;
-    sincospif(2.f * (float)turn, &s, &c);
-    cs[p] = make_float2(c * a.scale, (a.inverse ? -s : s) * a.scale);
+    const float most = (float)turn, rest = (float)(turn - (double)most) * 6.283185307179586f;
+    sincospif(2.f * most, &s, &c);
+    const float cos = fmaf(-s, rest, c), sin = fmaf(c, rest, s);
+    cs[p] = make_float2(cos * a.scale, (a.inverse ? -sin : sin) * a.scale);
   }
 }
 

@@ -1,5 +1,5 @@
-// glr.cuh -- what the kernels of the gated linear recurrence share: gates, four channels
-// at a time, spans of tokens and their exchange inside a cluster, sequences in packed rows.
+// glr.cuh -- the gates of the gated linear recurrence, four channels at a time, for the walk
+// over sequences (glr_scan.cuh) and the single token (glr_step.cu).
 #pragma once
 
 #include <float.h>

@@ -60,7 +60,7 @@ cudaError_t srem_reorient_launch(const void* x, void* y, int dir, int inverse, i
 cudaError_t dwconv3x3_launch(const void* x, const float* w, void* y, int B, int Hg, int Wg, int C, int dtype,
                              cudaStream_t st);
 
-// ---- gated linear recurrence (glr.cu, glr_step.cu) ----
+// ---- gated linear recurrence (glr_fwd.cu, glr_bwd.cu, glr_step.cu) ----
 // A batch of grids (cu == nullptr: B sequences of Hg * Wg tokens in scan order `dir`), or
 // packed sequences (B = 1, Hg = 1, Wg = rows; sequence n is rows cu[n] .. cu[n + 1] - 1,
 // dir 0 or 1).  Strides in elements between token rows; everything else is dense.

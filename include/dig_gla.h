@@ -270,8 +270,13 @@ int dwconv3x3(const void* x, const float* w, int B, int Hgrid, int Wgrid, int C,
  * the device status and the output is not valid.  NaN propagates along its channel to the
  * end of its sequence, as in the recurrence itself.
  *
+ * Limits (GLA_ERR_UNSUPPORTED beyond): C <= 65536; at most 2^24 sequences (states of a pool), and
+ * sequences * ceil(C / 64) <= 2^26; 2^30 tokens of a grid, or packed rows; strides of 2^32
+ * elements, and rows * stride <= 2^42.
+ *
  * glr_fwd runs B sequences, each over the Hgrid x Wgrid grid in scan order `dir` (0..11;
- * Hgrid = 1, dir = 0: plain token order).  No order costs copies, the zigzag ones neither.
+ * Hgrid = 1, dir = 0: plain token order).  No order costs copies, the zigzag ones neither;
+ * these are walked token by token (forward 1.6 times, backward 1.2 times the columns' time).
  */
 int glr_fwd(const void* x, const void* gate, const float* h0, int B, int Hgrid, int Wgrid, int C, int64_t x_stride,
             int64_t gate_stride, int dir, float gate_norm, int complement, int dtype, void* out, float* h_last,
@@ -319,6 +324,8 @@ int glr_bwd_packed(const void* x, const void* gate, const void* h, const void* d
  *             A slot >= nslots counts as padding and records GLA_ERR_INVALID_ARG.  Rows
  *             that name the same slot are its successive tokens, in row order.
  *   x, gate   N rows as above; out [N][C] of `dtype`, dense.  N <= 65535.
+ * With slots every row looks through all of them, so the time grows with the square of many rows
+ * (2048 channels: 4096 rows 21 us, 16384 rows 135 us, 65535 rows 1.7 ms).
  */
 int glr_step(const void* x, const void* gate, const float* state, const int* slots, int N, int nslots, int C,
              int64_t x_stride, int64_t gate_stride, float gate_norm, int complement, int dtype, int fill,
@@ -341,7 +348,8 @@ int glr_step(const void* x, const void* gate, const float* state, const int* slo
  *   q_out, k_out  rows like q and k with strides of their own; each may be its input (same
  *             pointer and stride), and overlaps no input otherwise.
  * D and rot are multiples of 8, 8 <= rot <= D <= 256; pointers and row strides are
- * multiples of 16 bytes; rows * (Hq + Hk) <= 2^31.
+ * multiples of 16 bytes; Hq, Hk <= 4096, rows * (Hq + Hk) <= 2^31; strides of at most 2^32
+ * elements, and rows * stride <= 2^42.
  */
 int rope(const void* q, const void* k, const void* positions, int positions64, int period, const float* inv_freq,
          int64_t rows, int Hq, int Hk, int D, int rot, int64_t q_stride, int64_t k_stride, int interleaved, int inverse,

@@ -72,10 +72,16 @@ __device__ __forceinline__ void decay(float2 x, float2& alpha, float2& rest) {
   p = __ffma2_rn(x, p, both(1.f / 6.f));
   p = __ffma2_rn(x, p, both(0.5f));
   p = __ffma2_rn(x, p, both(1.f));
-  const float2 close = __ffma2_rn(x, p, both(1.f)), less = __fmul2_rn(x, p), far = __ffma2_rn(ex, both(-1.f), both(1.f));
   const bool near_x = fabsf(x.x) < kNear, near_y = fabsf(x.y) < kNear;
+  float2 close;
+  if constexpr (kRest) {
+    const float2 less = __fmul2_rn(x, p);
+    rest = make_float2(near_x ? -less.x : 1.f - ex.x, near_y ? -less.y : 1.f - ex.y);
+    close = make_float2(1.f - rest.x, 1.f - rest.y);
+  } else {
+    close = __ffma2_rn(x, p, both(1.f));
+  }
   alpha = make_float2(near_x ? close.x : ex.x, near_y ? close.y : ex.y);
-  rest = make_float2(near_x ? -less.x : far.x, near_y ? -less.y : far.y);
 }
 
 // log(1 + e) for e in [0, 1], relative error 2e-7: e times the polynomial that interpolates
@@ -96,7 +102,7 @@ __device__ __forceinline__ float2 log_one_plus(float2 e) {
 // Two gates: alpha; 1 - alpha with its own relative accuracy; d log_alpha / d gate.  The
 // fields a caller does not use cost nothing once inlined.
 struct Gates {
-  float2 alpha, rest, slope;
+  float2 alpha{}, rest{}, slope{};
 };
 template <int kKind, bool kFine, bool kRest>
 __device__ __forceinline__ Gates make_gates(float2 g, float inv_norm) {

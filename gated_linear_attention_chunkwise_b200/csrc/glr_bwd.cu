@@ -121,15 +121,6 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
       }
       pull[i] = kKind == kGateLog ? before : mul4(before, k.slope);
     }
-    // Rows of no sequence pass on what enters them, whatever they hold.
-    if (packed && m.inside != (1u << kRun) - 1u) {
-#pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        if (m.inside >> i & 1u) continue;
-        al[i] = all4(1.f);
-        d[i] = all4(0.f);
-      }
-    }
     // The last token of a sequence takes dh_last in and forgets the token behind.
     Span s = nothing();
     if (m.last) {
@@ -149,11 +140,14 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
       for (int i = 0; i < kRun; ++i) s = Span{mul4(s.A, al[i]), mul4(al[i], add4(d[i], s.h))};
     }
     bool odd = !all_within(s.A, 1.f) || (packed && !modest(s.h));
-    if (n < kRun || odd) {  // the last round's end, growth, values that may not stay finite
+    // The last round's end, rows of no sequence (which pass on what enters them, whatever they
+    // hold), growth, values that may not stay finite.
+    const uint32_t there = packed ? m.inside : (1u << n) - 1u;
+    if (there != (1u << kRun) - 1u || odd) {
       s = nothing();
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
-        if (i >= n) {
+        if (!(there >> i & 1u)) {
           al[i] = all4(1.f);
           d[i] = all4(0.f);
         }
@@ -185,11 +179,10 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
       }
       continue;
     }
-    const uint32_t write = packed ? m.inside : (1u << n) - 1u;
     const int64_t row = rows.next(g), step = (int64_t)apart * a.C;
     T* px = dx + row * a.C;
     G* pg = dgate + row * a.C;
-    if (write == (1u << kRun) - 1u && (!packed || (m.first | m.last) == 0u)) {
+    if (there == (1u << kRun) - 1u && (!packed || (m.first | m.last) == 0u)) {
 #pragma unroll
       for (int i = 0; i < kRun; ++i) {
         const F4 delta = add4(d[i], r);
@@ -207,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 3) glr_bwd_k(GlrArgs a, ScanGeom g, 
       r = mul4(al[i], delta);
       if (packed && a.dh0 && (m.first >> i & 1u))
         store4(a.dh0 + state_row(a, m.first, i, m.first_seq, token(i)) + c, r);
-      if (write >> i & 1u) {
+      if (there >> i & 1u) {
         store4(px, kComp ? mul4(delta, keep[kComp ? i : 0]) : delta);
         store4(pg, mul4(r, pull[i]));
       } else if (a.fill && i < n) {

@@ -3,8 +3,9 @@
 // the walk is scan position T - 1 - j; what enters a span is r of the token behind it.
 //
 // Four tokens a thread, since a token needs four values a channel (alpha, d and the two
-// factors of the gradients): packed 32749 x 2048, logits and complement, 310 us; eight tokens
-// and two blocks an SM 314, four and four blocks (spilling) 349.
+// factors of the gradients): packed 32749 x 2048, logits and complement, 314 us; eight tokens
+// and two blocks an SM 316, four and four blocks (spilling) 362.  (With log_alpha alone both
+// would be faster: 64 sequences of 1024 x 2048 436 us, 398 and 379.)
 #include "glr_scan.cuh"
 
 namespace dig {

@@ -6,9 +6,9 @@ namespace dig {
 namespace glr {
 namespace {
 
-// Blocks an SM that the registers allow: with log_alpha four (128 registers, the c4 grid 62
-// instead of 68 us with three); the gates of the other forms would spill (packed, logits and
-// complement: 390 us with four, 341 with three).
+// Blocks an SM that the registers allow: with log_alpha four (128 registers, the c4 grid 65
+// instead of 67 us with three); the gates of the other forms would spill (packed, logits and
+// complement: 402 us with four, 347 with three).
 constexpr int resident(int kind, bool comp) { return kind == kGateLog && !comp ? 4 : 3; }
 
 template <typename T, int kKind, bool kComp, int kLanes, int kRun>

@@ -20,13 +20,13 @@
 // sign bit of A (gates are never negative): where a value is not finite the fold selects
 // instead of multiplying by zero, so a NaN ends with its sequence.
 //
-// What bounds it.  With log_alpha large calls reach 68-80 % of the copy bandwidth (64
-// sequences of 1024 x 2048 bf16: 206 us for 1.07 GB); with logits and the complement form the
-// gates take 16 of 40 instructions an element and it is 36-47 %, half of that issue and half
+// What bounds it.  With log_alpha large calls reach 64-81 % of the copy bandwidth (64
+// sequences of 1024 x 2048 bf16: 218 us for 1.07 GB); with logits and the complement form the
+// gates take 17 of 42 instructions an element and it is 35-45 %, half of that issue and half
 // the latency of a round's exchange.  Eight tokens a thread: with 4 the fixed work of a round
-// (330 instructions a thread) doubles an element (one 16384 x 2048 call 68 -> 86 us), with 16
-// the registers leave too few warps (packed, logits: 341 -> 373 us).  128 threads a block:
-// 64 take 385 us there, 96 take 348, 160 take 393, 256 take 377.
+// (330 instructions a thread) doubles an element (one 16384 x 2048 call 70 -> 87 us), with 16
+// the registers leave too few warps (packed, logits: 347 -> 376 us).  128 threads a block, with
+// as many warps an SM: 64 take 396 us there, 96 take 358, 256 take 409.
 #pragma once
 
 #include <algorithm>
@@ -438,7 +438,12 @@ struct Plan {
 // clusters and half the rounds, and win until the SMs are full (one sequence of 65536 tokens,
 // us wide / narrow with clusters of 8: 64 channels 146 / 75, 1024 channels 178 / 142, 2048
 // channels 242 / 257).  Each block above 8 adds 0.12 us to a round, so wider clusters pay
-// while SMs are idle (64 channels 75 -> 45, 256 channels 94 -> 68).
+// while SMs are idle (64 channels 75 -> 45, 256 channels 94 -> 68).  Other gates and the
+// backward have other rounds (predicted times are 0.9 to 1.7 times the measured ones), but the
+// order of the choices hardly changes: for ten shapes from 3 x 777 x 136 to one sequence of
+// 65536 x 2048 and 64 of 1024 x 2048, each forwards and backwards with log_alpha and with logits
+// and complement, all slabs and cluster sizes were timed.  In 39 of the 40 the choice was
+// within 2 % of the fastest, in one (1 us of 9) within 13 %.
 inline cudaError_t plan(Kernel k, Known& known, const GlrArgs& a, const ScanGeom& g, int lanes, int run, size_t smem,
                         Plan* best) {
   int dev = 0;
@@ -465,7 +470,9 @@ inline cudaError_t plan(Kernel k, Known& known, const GlrArgs& a, const ScanGeom
   return cudaSuccess;
 }
 
-// The cheaper of the kernels with 32- and with 16-channel slabs.
+// The cheaper of the kernels with 32- and with 16-channel slabs.  Beyond 2^20 channels of
+// sequences clusters of one block fill the SMs many times over and wide slabs win: 30000 x 64
+// tokens of 40 channels 705 us wide, 1061 narrow; of 16 channels, half a slab, 827 and 788.
 inline cudaError_t enqueue(Kernel wide, Known& known_wide, Kernel narrow, Known& known_narrow, const GlrArgs& a, int run,
                            size_t smem, cudaStream_t st) {
   const ScanGeom g = make_geom(a.Hg, a.Wg, a.dir);

@@ -7,10 +7,10 @@
 //
 // Bound: memory; every head is read and written once (the gradient: two reads, one write).
 // Measured, of the copy bandwidth: rotation of bf16 heads 88 % (16381 tokens of 40 heads of
-// 128: 58 us), with the norm 73 % (70 us), of fp32 heads 77 % (8191 tokens of 32 heads of 80:
-// 33 us) and 86 %.  What keeps the norm from more is instruction issue (64 % of the cycles:
+// 128: 58 us), with the norm 71 % (72 us), of fp32 heads 77 % (8191 tokens of 32 heads of 80:
+// 33 us) and 86 %.  What keeps the norm from more is instruction issue (63 % of the cycles:
 // unpacking, two passes over a head's channels around the sum, the packing).  The gradient
-// reaches 42 % with 72 channels and 60 % with 128 (25088 tokens of 32 heads of 72: 124 us):
+// reaches 42 % with 72 channels and 60 % with 128 (25088 tokens of 32 heads of 72: 125 us):
 // twice the work of a head, 16 warps an SM, 27 of 32 lanes at 72 channels.
 //
 // Split.  Eight channels that rotate among themselves are a unit: quads i and i + rot / 8
